@@ -74,6 +74,7 @@ typedef enum { EKV_F32 = 0, EKV_BF16 = 1 } ekv_dtype;
 #define EKV_EFLAG_SEL_OVERFLOW 4u  /* Gaussian policy kept more than cap pages */
 #define EKV_EFLAG_BAD_SEL 8u       /* sel entry outside [0, pages of the sequence) */
 #define EKV_EFLAG_TIMEOUT 16u      /* a bounded wait on an asynchronous copy gave up */
+#define EKV_EFLAG_BAD_POS 32u      /* a token's position has no row in the rotation table */
 
 /* The paged KV cache and its per-page metadata pools (all device memory). */
 typedef struct {
@@ -204,6 +205,160 @@ EKV_API ekv_status ekv_softmax_decode(const ekv_cache* cache, const ekv_seqs* se
                                       int32_t num_q_heads, float scale, const int32_t* sel,
                                       const int32_t* n_sel, int32_t cap, float* out, float* lse,
                                       void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Rotary position embedding.  Pairs (x1, x2) of the first rot_dim coordinates
+ * of a head become (x1·c − x2·s, x2·c + x1·s) with the cosine c and sine s of
+ * the token's position; the other coordinates pass unchanged.  The pairs are
+ * (j, j + rot_dim/2), or (2j, 2j + 1) when interleaved ≠ 0.  The angles are
+ * the caller's: row p of the table holds the rot_dim/2 cosines of position p,
+ * then its rot_dim/2 sines (any frequency scaling is in the table).
+ */
+typedef struct {
+  const float* cos_sin; /* device fp32 [max_pos, rot_dim], 16-byte aligned */
+  int32_t max_pos;      /* rows; a token at a position ≥ max_pos is rotated by the
+                           last row and raises EKV_EFLAG_BAD_POS */
+  int32_t rot_dim;      /* a multiple of 16, 16 ≤ rot_dim ≤ d */
+  int32_t interleaved;
+} ekv_rope;
+
+/*
+ * New tokens of a batch, one row per token.  Rows indptr[b] .. indptr[b+1]−1
+ * are the last n_b = indptr[b+1] − indptr[b] tokens of sequence b, at positions
+ * L_b − n_b .. L_b − 1 (seq_lens already counts them; n_b = 0 leaves the
+ * sequence alone).  Rows at and past indptr[batch] are neither read nor
+ * written.  A row holds its heads densely ([Hkv, d] or [Hq, d]); the rows may
+ * be strided, so the three can be views of one fused projection.
+ */
+typedef struct {
+  const void* q;         /* device, cache dtype; NULL: no queries to rotate */
+  const void* k;
+  const void* v;
+  void* q_out;           /* device [num_tokens, Hq, d] dense; may be q itself */
+  int64_t q_stride;      /* elements from one token's row to the next */
+  int64_t k_stride;
+  int64_t v_stride;
+  const int32_t* indptr; /* device [batch + 1], nondecreasing; NULL: one token per sequence */
+  int32_t num_tokens;    /* rows of q, k, v and q_out */
+  int32_t num_q_heads;   /* Hq (ignored when q is NULL) */
+  int32_t dtype;         /* ekv_dtype of q, k, v and q_out */
+} ekv_new_tokens;
+
+/*
+ * ekv_rope_append — the cache append of a decode step, a prompt or a chunk of
+ * one, with the rotation applied on the way.  Rotates k (rope NULL: no
+ * rotation) and writes it and v to the tokens' places in the pages; rotates q
+ * into q_out; recomputes box/mom of every page that received a token over its
+ * valid tokens, exactly as ekv_build_page_meta does (of the keys as stored;
+ * [EntmaxKV] §2.A).  box and mom may both be NULL: no metadata is kept then.
+ * The rotation runs in fp32 and is rounded once to the cache dtype.  dtype
+ * must be the cache's.  Row pointers are 16-byte aligned and strides a
+ * multiple of 16 bytes (else EKV_ERR_INVALID_ARG).  A sequence whose indptr
+ * entries or length are inconsistent (n_b > L_b, L_b > max_pages·S, rows past
+ * num_tokens) is skipped and raises EKV_EFLAG_BAD_LEN; L_b = 0 with n_b = 0 is
+ * an idle slot and raises nothing.
+ */
+EKV_API ekv_status ekv_rope_append(const ekv_cache* cache, const ekv_seqs* seqs, const ekv_rope* rope,
+                                   const ekv_new_tokens* tokens, void* stream);
+
+/*
+ * A paged cache held in 4 bits.  pool: [num_phys_pages, Hkv, S/16, R] bytes,
+ * one record of R = 16·d + 128 bytes per 16 tokens: the K codes [16, d/2]
+ * (coordinate 2i in the low half of byte i), the V codes [16, d/2], 16 pairs
+ * (step, zero) in bf16 for K, 16 for V.  A row x of d numbers has
+ *   zero = bf16(min x), step = bf16((max x − min x)/15) (0 below 1e-30),
+ *   n_j = clamp(round((x_j − zero)/step), 0, 15)   (halves to the even code),
+ * and stands for zero + step·n_j.  box and mom as in ekv_cache, always bf16,
+ * over the values the codes stand for; k_max is rounded up and k_min down, so
+ * the bounding-box bound stays a bound.  To score pages, pass an ekv_cache of
+ * dtype EKV_BF16 with the same sizes, box and mom to ekv_score_pages or
+ * ekv_select_gauss (they read no K).
+ */
+typedef struct {
+  int32_t head_dim;       /* d ∈ {64, 128} */
+  int32_t page_size;      /* S ∈ {16, 32} */
+  int32_t num_kv_heads;
+  int32_t num_phys_pages;
+  void* pool;             /* device, 16-byte aligned */
+  void* box;              /* device, nullable together with mom */
+  void* mom;
+} ekv_cache_q4;
+
+/*
+ * ekv_rope_append_q4 — ekv_rope_append into a 4-bit cache.  tokens->dtype is
+ * EKV_BF16 or EKV_F32 (q_out has it too).  The codes are those of the exact
+ * rotated row: borders between two codes are decided in 64 bits.
+ */
+EKV_API ekv_status ekv_rope_append_q4(const ekv_cache_q4* cache, const ekv_seqs* seqs, const ekv_rope* rope,
+                                      const ekv_new_tokens* tokens, void* stream);
+
+/*
+ * ekv_q4_read — reads tokens of a 4-bit cache back as values: row
+ * indptr[b] + i of k_out / v_out (device [num_tokens, Hkv, d] dense, out_dtype,
+ * 16-byte aligned, either may be NULL) is token L_b − n_b + i of sequence b,
+ * zero + step·n rounded to fp32 (and from there to bf16).  indptr (device
+ * [batch + 1], not NULL) and its checks are those of ekv_new_tokens; rows it
+ * does not name are left as they were.
+ */
+EKV_API ekv_status ekv_q4_read(const ekv_cache_q4* cache, const ekv_seqs* seqs, const int32_t* indptr,
+                               int32_t num_tokens, int32_t out_dtype, void* k_out, void* v_out, void* stream);
+
+/*
+ * How scores are capped, biased and masked.  For the query token at position
+ * i and the token at position j, with z = scale·q·k_j:
+ *   s = softcap·tanh(z / softcap) (softcap > 0; s = z for softcap = 0)
+ *       − slopes[hq]·|i − j|       (slopes not NULL),
+ * and j is visible when j ≥ starts[b] and (j < prefix_lens[b] or (j ≤ i and
+ * (window = 0 or i − j < window))).  NULL starts / prefix_lens count as 0.
+ * Positions are those of the sequence, from 0; starts[b] is the first token
+ * of the query's own document.
+ */
+typedef struct {
+  float softcap;
+  int32_t window;
+  const float* slopes;        /* device fp32 [Hq], finite, nullable */
+  const int32_t* prefix_lens; /* device [batch], nullable */
+  const int32_t* starts;      /* device [batch], nullable */
+} ekv_score_mod;
+
+/*
+ * ekv_softmax_decode_mod — ekv_softmax_decode with capped, biased and masked
+ * scores, for num_q_tokens query tokens per sequence: the last T tokens of it,
+ * query t at position i = L_b − T + t (a draft's tokens checked at once).
+ * q: device [batch, T, Hq, d] in the cache dtype, 16-byte aligned; out: fp32
+ * [batch, T, Hq, d], 16-byte aligned; lse (nullable): fp32 [batch, T, Hq].
+ * mod may be NULL (causal, nothing else).  sel / n_sel / cap as
+ * ekv_softmax_decode; a page named twice counts twice.  Only pages with a
+ * visible token are read.  A row without a visible token (also L_b = 0, an
+ * idle slot, and i < 0) gives out 0 and lse −inf.  K and V of tokens that a
+ * row does not see never reach it, NaN and infinities included.  bf16 caches,
+ * G·T ≤ 64; anything else returns EKV_ERR_UNSUPPORTED.  ws:
+ * ekv_softmax_mod_workspace_bytes() bytes, 256-byte aligned, for one call at a
+ * time; nothing in it outlives the call.
+ */
+EKV_API ekv_status ekv_softmax_decode_mod(const ekv_cache* cache, const ekv_seqs* seqs, const void* q,
+                                          int32_t num_q_heads, int32_t num_q_tokens, float scale,
+                                          const ekv_score_mod* mod, const int32_t* sel, const int32_t* n_sel,
+                                          int32_t cap, float* out, float* lse, void* ws, size_t ws_bytes,
+                                          void* stream);
+
+/*
+ * ekv_softmax_decode_q4 — ekv_softmax_decode_mod over a 4-bit cache: K and V
+ * are the values the codes stand for (not rounded further).  q is bf16.
+ */
+EKV_API ekv_status ekv_softmax_decode_q4(const ekv_cache_q4* cache, const ekv_seqs* seqs, const void* q,
+                                         int32_t num_q_heads, int32_t num_q_tokens, float scale,
+                                         const ekv_score_mod* mod, const int32_t* sel, const int32_t* n_sel,
+                                         int32_t cap, float* out, float* lse, void* ws, size_t ws_bytes,
+                                         void* stream);
+
+/*
+ * Device scratch of ekv_softmax_decode_mod and ekv_softmax_decode_q4 (both
+ * alike; it depends on no batch size or length).  0 when the sizes are
+ * invalid or unsupported.
+ */
+EKV_API size_t ekv_softmax_mod_workspace_bytes(int32_t head_dim, int32_t num_kv_heads, int32_t num_q_heads,
+                                               int32_t num_q_tokens);
 
 /*
  * ekv_exactness_certificate — [EKV] §3 "Récupération du Support": the sparse

@@ -22,7 +22,10 @@ __all__ = [
     "ekv_decode_step", "ekv_workspace_bytes", "ekv_get_error", "ekv_status_string",
     "ekv_entmax_decode_static_ws", "ekv_step_kernel_count", "ekv_softmax_decode", "EKV_OP_SOFTMAX_DECODE",
     "ekv_exactness_certificate", "EKV_OP_SELECT_TOPK", "ekv_selftest_wait_timeout", "EKV_EFLAG_TIMEOUT",
-    "ekv_decode_adaptive", "EKV_OP_DECODE_ADAPTIVE",
+    "ekv_decode_adaptive", "EKV_OP_DECODE_ADAPTIVE", "EKV_EFLAG_BAD_POS",
+    "CacheQ4", "Rope", "NewTokens", "ScoreMod", "make_cache_q4", "make_rope", "make_new_tokens", "make_score_mod",
+    "q4_record_bytes", "ekv_rope_append", "ekv_rope_append_q4", "ekv_q4_read", "ekv_softmax_decode_mod",
+    "ekv_softmax_decode_q4", "ekv_softmax_mod_workspace_bytes",
 ]
 
 EKV_F32, EKV_BF16 = 0, 1
@@ -32,6 +35,7 @@ EKV_OP_SELECT_TOPK = 5
 EKV_OP_DECODE_ADAPTIVE = 6
 EKV_EFLAG_BAD_PAGE, EKV_EFLAG_BAD_LEN, EKV_EFLAG_SEL_OVERFLOW, EKV_EFLAG_BAD_SEL = 1, 2, 4, 8
 EKV_EFLAG_TIMEOUT = 16
+EKV_EFLAG_BAD_POS = 32
 
 lib_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libekv.so")
 
@@ -64,6 +68,29 @@ class StepParams(ctypes.Structure):
                 ("dense_v", ctypes.c_int32), ("append", ctypes.c_int32)]
 
 
+class CacheQ4(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("num_phys_pages", ctypes.c_int32), ("pool", ctypes.c_void_p), ("box", ctypes.c_void_p),
+                ("mom", ctypes.c_void_p)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
+
+
+class NewTokens(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("indptr", ctypes.c_void_p), ("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class ScoreMod(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p), ("starts", ctypes.c_void_p)]
+
+
 _LIB = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
@@ -86,6 +113,16 @@ _SIGS = {
     "ekv_exactness_certificate": [ctypes.POINTER(Seqs), _I, _I, _I, _F, _P, _P, _P, _I, _P, _P, _P],
     "ekv_decode_adaptive": [ctypes.POINTER(Cache), ctypes.POINTER(Seqs), _P, _I, _F, _F, _I, _P, _P, _P, _P, _P,
                             ctypes.POINTER(ctypes.c_int32), _P, _SZ, _P],
+    "ekv_rope_append": [ctypes.POINTER(Cache), ctypes.POINTER(Seqs), ctypes.POINTER(Rope), ctypes.POINTER(NewTokens),
+                        _P],
+    "ekv_rope_append_q4": [ctypes.POINTER(CacheQ4), ctypes.POINTER(Seqs), ctypes.POINTER(Rope),
+                           ctypes.POINTER(NewTokens), _P],
+    "ekv_q4_read": [ctypes.POINTER(CacheQ4), ctypes.POINTER(Seqs), _P, _I, _I, _P, _P, _P],
+    "ekv_softmax_decode_mod": [ctypes.POINTER(Cache), ctypes.POINTER(Seqs), _P, _I, _I, _F, ctypes.POINTER(ScoreMod),
+                               _P, _P, _I, _P, _P, _P, _SZ, _P],
+    "ekv_softmax_decode_q4": [ctypes.POINTER(CacheQ4), ctypes.POINTER(Seqs), _P, _I, _I, _F,
+                              ctypes.POINTER(ScoreMod), _P, _P, _I, _P, _P, _P, _SZ, _P],
+    "ekv_softmax_mod_workspace_bytes": [_I, _I, _I, _I],
     "ekv_selftest_wait_timeout": [ctypes.c_uint32, _P],
     "ekv_step_kernel_count": [ctypes.POINTER(Cache), ctypes.POINTER(Seqs), ctypes.POINTER(StepParams), _I],
     "ekv_entmax_decode_static_ws": [ctypes.POINTER(Cache), ctypes.POINTER(Seqs), _P, _I, _F, _F, _P,
@@ -110,6 +147,7 @@ def lib():
             fn.argtypes = args
             fn.restype = ctypes.c_int32
         h.ekv_workspace_bytes.restype = ctypes.c_size_t
+        h.ekv_softmax_mod_workspace_bytes.restype = ctypes.c_size_t
         h.ekv_status_string.restype = ctypes.c_char_p
         _LIB = h
     return _LIB
@@ -166,6 +204,98 @@ def make_seqs(page_table, seq_lens) -> Seqs:
     s = Seqs(page_table.data_ptr(), seq_lens.data_ptr(), page_table.shape[0], page_table.shape[1])
     s._keep = (page_table.contiguous(), seq_lens.contiguous())
     return s
+
+
+def q4_record_bytes(head_dim: int) -> int:
+    """Bytes of a 4-bit cache's record: 16 tokens of one (page, KV head), K and V."""
+    return 16 * head_dim + 128
+
+
+def make_cache_q4(pool, head_dim, box=None, mom=None) -> CacheQ4:
+    """Describe a 4-bit cache.  pool: uint8 [num_phys, Hkv, S/16, q4_record_bytes(head_dim)];
+    box, mom: bf16 [Hkv, num_phys, 2, d] (both None: no metadata is kept).  With
+    metadata, ``.meta`` is the bf16 cache description that ekv_score_pages and
+    ekv_select_gauss take (they read no K)."""
+    if pool.dtype != torch.uint8 or pool.dim() != 4 or pool.shape[3] != q4_record_bytes(head_dim):
+        raise ValueError(f"pool must be uint8 [num_phys, Hkv, S/16, {q4_record_bytes(head_dim)}]")
+    if (box is None) != (mom is None):
+        raise ValueError("box and mom come together")
+    for t in (box, mom):
+        if t is not None and (t.dtype != torch.bfloat16
+                              or tuple(t.shape) != (pool.shape[1], pool.shape[0], 2, head_dim)):
+            raise ValueError("box and mom must be bf16 [Hkv, num_phys, 2, d]")
+    keep = [t for t in (pool, box, mom) if t is not None]
+    _same_device(*keep)
+    if not all(t.is_contiguous() for t in keep):
+        raise ValueError("cache tensors must be contiguous")
+    ptrs = [0 if t is None else t.data_ptr() for t in (pool, box, mom)]
+    c = CacheQ4(head_dim, 16 * pool.shape[2], pool.shape[1], pool.shape[0], *ptrs)
+    c._keep, c.box_t, c.mom_t, c.device = keep, box, mom, pool.device
+    if box is not None:
+        c.meta = Cache(EKV_BF16, head_dim, c.page_size, c.num_kv_heads, c.num_phys_pages, ptrs[0], ptrs[0], *ptrs[1:])
+        c.meta._keep, c.meta.box_t, c.meta.mom_t = keep, box, mom
+    return c
+
+
+def make_rope(cos_sin, interleaved=False) -> Rope:
+    """cos_sin: fp32 [positions, rot_dim], a row's cosines, then its sines."""
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be contiguous fp32 [positions, rot_dim]")
+    r = Rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)))
+    r._keep, r.device = cos_sin, cos_sin.device
+    return r
+
+
+def make_new_tokens(k, v, q=None, q_out=None, indptr=None) -> NewTokens:
+    """k, v: [tokens, Hkv, d] and q: [tokens, Hq, d], rows strided as one likes,
+    heads dense; q_out: dense [tokens, Hq, d]; indptr: int32 [B + 1] (None: one
+    token per sequence)."""
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if k.shape != v.shape or k.dim() != 3:
+        raise ValueError("k and v must be [tokens, Hkv, d]")
+    rows = [t for t in (k, v, q, q_out) if t is not None]
+    for t in rows:
+        if t.dtype != k.dtype or t.dtype not in _DTYPES or t.shape[0] != k.shape[0] or t.shape[2] != k.shape[2]:
+            raise ValueError("q, k, v and q_out must share their type, tokens and head size")
+        if t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+            raise ValueError("the heads of a token must be dense")
+    if q is not None and (q.shape != q_out.shape or not q_out.is_contiguous()):
+        raise ValueError("q_out must be dense, of q's shape")
+    if indptr is not None and (indptr.dtype != torch.int32 or indptr.dim() != 1 or not indptr.is_contiguous()):
+        raise ValueError("indptr must be int32 [batch + 1]")
+    _same_device(*rows, *([] if indptr is None else [indptr]))
+    pq = (lambda t: 0 if t is None else t.data_ptr())
+    n = NewTokens(pq(q), k.data_ptr(), v.data_ptr(), pq(q_out), 0 if q is None else q.stride(0), k.stride(0),
+                  v.stride(0), pq(indptr), k.shape[0], 0 if q is None else q.shape[1], _DTYPES[k.dtype])
+    n._keep, n.device, n.shape = (rows, indptr), k.device, (k.shape[1], k.shape[2])
+    return n
+
+
+def make_score_mod(softcap=0.0, slopes=None, window=0, prefix_lens=None, starts=None) -> ScoreMod:
+    """How scores are capped, biased and masked (include/ekv.h, ekv_score_mod).
+    slopes: fp32 [Hq]; prefix_lens, starts: int32 [B]."""
+    for t, dt in ((slopes, torch.float32), (prefix_lens, torch.int32), (starts, torch.int32)):
+        if t is not None and (t.dtype != dt or t.dim() != 1 or not t.is_contiguous()):
+            raise ValueError("slopes must be fp32 [Hq], prefix_lens and starts int32 [batch]")
+    keep = [t for t in (slopes, prefix_lens, starts) if t is not None]
+    if keep:
+        _same_device(*keep)
+    ptr = (lambda t: 0 if t is None else t.data_ptr())
+    m = ScoreMod(float(softcap or 0.0), int(window or 0), ptr(slopes), ptr(prefix_lens), ptr(starts))
+    m._keep = (slopes, prefix_lens, starts)
+    return m
+
+
+def _same_device(*tensors):
+    if any(t.device != tensors[0].device for t in tensors):
+        raise ValueError("all tensors must be on one device")
+
+
+def _on_current(device):
+    """Kernels launch on the current device: another one's tensors are refused."""
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {device}, which is not the current CUDA device")
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
@@ -247,6 +377,100 @@ def ekv_decode_adaptive(cache, seqs, q, scale, alpha, k0, sel, n_sel, out, tau, 
         _ptr(out), _ptr(tau), _ptr(certified), ctypes.byref(k_used), _ptr(ws), 0 if ws is None else ws.numel(),
         _stream(stream)))
     return int(k_used.value)
+
+
+def _check_append(cache_device, heads, seqs, rope, new):
+    _on_current(new.device)
+    if cache_device != new.device or (rope is not None and rope.device != new.device):
+        raise ValueError("all tensors must be on one device")
+    if new.shape != heads:
+        raise ValueError(f"new tokens have [Hkv, d] = {new.shape}, the cache {heads}")
+    indptr = new._keep[1]
+    if indptr is not None and indptr.numel() != seqs.batch + 1:
+        raise ValueError("indptr must have batch + 1 entries")
+
+
+def ekv_rope_append(cache, seqs, rope, new, stream=None):
+    """Rotate and append new tokens (rope None: no rotation); see include/ekv.h."""
+    _check_append(cache.box_t.device, (cache.num_kv_heads, cache.head_dim), seqs, rope, new)
+    _check("ekv_rope_append", lib().ekv_rope_append(
+        ctypes.byref(cache), ctypes.byref(seqs), None if rope is None else ctypes.byref(rope), ctypes.byref(new),
+        _stream(stream)))
+
+
+def ekv_rope_append_q4(cache, seqs, rope, new, stream=None):
+    """ekv_rope_append into a 4-bit cache."""
+    _check_append(cache.device, (cache.num_kv_heads, cache.head_dim), seqs, rope, new)
+    _check("ekv_rope_append_q4", lib().ekv_rope_append_q4(
+        ctypes.byref(cache), ctypes.byref(seqs), None if rope is None else ctypes.byref(rope), ctypes.byref(new),
+        _stream(stream)))
+
+
+def ekv_q4_read(cache, seqs, indptr, k_out=None, v_out=None, stream=None):
+    """Read tokens of a 4-bit cache back as values.  k_out, v_out: fp32 or bf16
+    [tokens, Hkv, d], dense, either None; indptr: int32 [batch + 1], the rows of
+    each sequence's last tokens."""
+    outs = [t for t in (k_out, v_out) if t is not None]
+    if not outs:
+        raise ValueError("k_out or v_out is needed")
+    for t in outs:
+        if t.dtype not in _DTYPES or t.dtype != outs[0].dtype or not t.is_contiguous() or t.shape != outs[0].shape \
+                or tuple(t.shape[1:]) != (cache.num_kv_heads, cache.head_dim):
+            raise ValueError("k_out and v_out must be dense fp32 or bf16 [tokens, Hkv, d]")
+    if indptr.dtype != torch.int32 or not indptr.is_contiguous() or indptr.numel() != seqs.batch + 1:
+        raise ValueError("indptr must be int32 [batch + 1]")
+    _on_current(cache.device)
+    _same_device(indptr, *outs, cache._keep[0])
+    _check("ekv_q4_read", lib().ekv_q4_read(
+        ctypes.byref(cache), ctypes.byref(seqs), _ptr(indptr), outs[0].shape[0], _DTYPES[outs[0].dtype], _ptr(k_out),
+        _ptr(v_out), _stream(stream)))
+
+
+def ekv_softmax_mod_workspace_bytes(head_dim, num_kv_heads, num_q_heads, num_q_tokens=1) -> int:
+    return int(lib().ekv_softmax_mod_workspace_bytes(head_dim, num_kv_heads, num_q_heads, num_q_tokens))
+
+
+def _softmax_mod(name, cache, device, seqs, q, scale, mod, sel, n_sel, cap, out, ws, lse, stream):
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be dense bf16 [batch, T, Hq, d]")
+    if q.shape[0] != seqs.batch or q.shape[3] != cache.head_dim:
+        raise ValueError("q does not fit the batch and the cache")
+    if out.shape != q.shape or out.dtype != torch.float32 or not out.is_contiguous():
+        raise ValueError("out must be dense fp32 of q's shape")
+    if lse is not None and (lse.shape != q.shape[:3] or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be dense fp32 [batch, T, Hq]")
+    if sel is not None and (sel.dtype != torch.int32 or not sel.is_contiguous()
+                            or tuple(sel.shape) != (seqs.batch, cache.num_kv_heads, cap)):
+        raise ValueError("sel must be dense int32 [batch, Hkv, cap]")
+    if n_sel is not None and (n_sel.dtype != torch.int32 or n_sel.numel() != seqs.batch * cache.num_kv_heads
+                              or not n_sel.is_contiguous()):
+        raise ValueError("n_sel must be dense int32 [batch, Hkv]")
+    if mod is not None:
+        slopes, prefix_lens, starts = mod._keep
+        if slopes is not None and slopes.numel() != q.shape[2]:
+            raise ValueError("slopes must have one entry per query head")
+        if any(t is not None and t.numel() != seqs.batch for t in (prefix_lens, starts)):
+            raise ValueError("prefix_lens and starts must have one entry per sequence")
+    _on_current(device)
+    _same_device(cache._keep[0], q, out, ws, *(t for t in (lse, sel, n_sel) if t is not None),
+                 *(t for t in (mod._keep if mod is not None else ()) if t is not None))
+    _check(name, getattr(lib(), name)(
+        ctypes.byref(cache), ctypes.byref(seqs), _ptr(q), q.shape[2], q.shape[1], scale,
+        None if mod is None else ctypes.byref(mod), _ptr(sel), _ptr(n_sel), cap, _ptr(out), _ptr(lse), _ptr(ws),
+        ws.numel(), _stream(stream)))
+
+
+def ekv_softmax_decode_mod(cache, seqs, q, scale, mod, sel, n_sel, cap, out, ws, *, lse=None, stream=None):
+    """Softmax decode with capped, biased and masked scores (mod: make_score_mod,
+    or None) for the last T tokens of every sequence.  q: bf16 [B, T, Hq, d]."""
+    _softmax_mod("ekv_softmax_decode_mod", cache, cache.box_t.device, seqs, q, scale, mod, sel, n_sel, cap, out, ws,
+                 lse, stream)
+
+
+def ekv_softmax_decode_q4(cache, seqs, q, scale, mod, sel, n_sel, cap, out, ws, *, lse=None, stream=None):
+    """ekv_softmax_decode_mod over a 4-bit cache."""
+    _softmax_mod("ekv_softmax_decode_q4", cache, cache.device, seqs, q, scale, mod, sel, n_sel, cap, out, ws, lse,
+                 stream)
 
 
 def ekv_selftest_wait_timeout(polls=1024, stream=None):

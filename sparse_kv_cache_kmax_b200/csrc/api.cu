@@ -163,6 +163,72 @@ ekv_status validate_decode(const ekv_cache* cache, const ekv_seqs* seqs, const v
   return EKV_OK;
 }
 
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// The sizes and metadata of a 4-bit cache as a bf16 cache without pools.
+ekv_cache q4_shape(const ekv_cache_q4* c) {
+  ekv_cache m{};
+  m.dtype = EKV_BF16;
+  m.head_dim = c->head_dim;
+  m.page_size = c->page_size;
+  m.num_kv_heads = c->num_kv_heads;
+  m.num_phys_pages = c->num_phys_pages;
+  m.k_pool = c->pool;
+  m.v_pool = c->pool;
+  m.box = c->box;
+  m.mom = c->mom;
+  return m;
+}
+
+ekv_status check_q4(const ekv_cache_q4* c) {
+  if (c == nullptr) return EKV_ERR_INVALID_ARG;
+  const ekv_cache m = q4_shape(c);
+  EKV_TRY(check_cache(&m, true, false));
+  return aligned16(c->pool) ? EKV_OK : EKV_ERR_INVALID_ARG;
+}
+
+ekv_status check_rope_append(const ekv_cache& c, const ekv_seqs* seqs, const ekv_rope* rope,
+                             const ekv_new_tokens* n) {
+  EKV_TRY(check_seqs(seqs));
+  if (n == nullptr || n->k == nullptr || n->v == nullptr) return EKV_ERR_INVALID_ARG;
+  if (n->dtype != EKV_F32 && n->dtype != EKV_BF16) return EKV_ERR_UNSUPPORTED;
+  if ((c.box == nullptr) != (c.mom == nullptr)) return EKV_ERR_INVALID_ARG;
+  if (n->num_tokens < (n->indptr == nullptr ? seqs->batch : 1)) return EKV_ERR_INVALID_ARG;
+  if (c.num_kv_heads > 32767 || seqs->batch > (1 << 28)) return EKV_ERR_UNSUPPORTED;
+  if (rope != nullptr) {
+    if (rope->cos_sin == nullptr || rope->max_pos < 1 || !aligned16(rope->cos_sin)) return EKV_ERR_INVALID_ARG;
+    if (rope->rot_dim < 16 || rope->rot_dim > c.head_dim || rope->rot_dim % 16 != 0) return EKV_ERR_INVALID_ARG;
+  }
+  const int64_t el = n->dtype == EKV_BF16 ? 2 : 4, d = c.head_dim;
+  auto rows_ok = [&](const void* p, int64_t stride, int64_t heads) {
+    return aligned16(p) && stride >= heads * d && stride * el % 16 == 0;
+  };
+  if (!rows_ok(n->k, n->k_stride, c.num_kv_heads) || !rows_ok(n->v, n->v_stride, c.num_kv_heads))
+    return EKV_ERR_INVALID_ARG;
+  if (n->q != nullptr) {
+    EKV_TRY(check_heads(&c, n->num_q_heads));
+    if (n->q_out == nullptr || !aligned16(n->q_out) || !rows_ok(n->q, n->q_stride, n->num_q_heads))
+      return EKV_ERR_INVALID_ARG;
+    if (n->q == n->q_out && n->q_stride != n->num_q_heads * d) return EKV_ERR_INVALID_ARG;
+  }
+  return EKV_OK;
+}
+
+ekv_status softmax_mod(const ekv_cache& c, const void* pool, const ekv_seqs* seqs, const void* q, int32_t Hq,
+                       int32_t T, float scale, const ekv_score_mod* mod, const int32_t* sel, const int32_t* n_sel,
+                       int32_t cap, float* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  EKV_TRY(validate_decode(&c, seqs, q, Hq, scale, 1.5f, sel, n_sel, cap, out));
+  if (T < 1) return EKV_ERR_INVALID_ARG;
+  if (c.dtype != EKV_BF16 || T > kModMaxRows || Hq / c.num_kv_heads * T > kModMaxRows) return EKV_ERR_UNSUPPORTED;
+  // rows of the pools are counted in 32 bits
+  if (static_cast<int64_t>(c.num_phys_pages) * c.num_kv_heads * c.page_size > INT32_MAX) return EKV_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(c.k_pool) || !aligned16(c.v_pool)) return EKV_ERR_INVALID_ARG;
+  if (mod != nullptr && (!isfinite(mod->softcap) || mod->softcap < 0.0f || mod->window < 0)) return EKV_ERR_INVALID_ARG;
+  EKV_TRY(check_ws(ws, ws_bytes, softmax_mod_ws_bytes(c.head_dim, Hq / c.num_kv_heads * T)));
+  return cuda_status(launch_softmax_mod(c, pool, *seqs, q, Hq, T, scale, mod, sel, n_sel, cap, out, lse, ws,
+                                        static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 }  // namespace ekv
 
@@ -318,6 +384,62 @@ EKV_API ekv_status ekv_softmax_decode(const ekv_cache* cache, const ekv_seqs* se
                                                   cache->head_dim, cap)));
   return cuda_status(launch_softmax_decode(*cache, *seqs, q, num_q_heads, scale, sel, n_sel, cap, out,
                                            lse, ws, static_cast<cudaStream_t>(stream)));
+}
+
+EKV_API ekv_status ekv_rope_append(const ekv_cache* cache, const ekv_seqs* seqs, const ekv_rope* rope,
+                                   const ekv_new_tokens* tokens, void* stream) {
+  EKV_TRY(check_cache(cache, true, false));
+  EKV_TRY(check_rope_append(*cache, seqs, rope, tokens));
+  if (tokens->dtype != cache->dtype || !aligned16(cache->k_pool) || !aligned16(cache->v_pool))
+    return EKV_ERR_INVALID_ARG;
+  return cuda_status(launch_rope_append(*cache, *seqs, rope, *tokens, static_cast<cudaStream_t>(stream)));
+}
+
+EKV_API ekv_status ekv_rope_append_q4(const ekv_cache_q4* cache, const ekv_seqs* seqs, const ekv_rope* rope,
+                                      const ekv_new_tokens* tokens, void* stream) {
+  EKV_TRY(check_q4(cache));
+  EKV_TRY(check_rope_append(q4_shape(cache), seqs, rope, tokens));
+  return cuda_status(launch_rope_append_q4(*cache, *seqs, rope, *tokens, static_cast<cudaStream_t>(stream)));
+}
+
+EKV_API ekv_status ekv_q4_read(const ekv_cache_q4* cache, const ekv_seqs* seqs, const int32_t* indptr,
+                               int32_t num_tokens, int32_t out_dtype, void* k_out, void* v_out, void* stream) {
+  EKV_TRY(check_q4(cache));
+  EKV_TRY(check_seqs(seqs));
+  if (out_dtype != EKV_F32 && out_dtype != EKV_BF16) return EKV_ERR_UNSUPPORTED;
+  if (cache->num_kv_heads > 65535 || seqs->batch > (1 << 28)) return EKV_ERR_UNSUPPORTED;
+  if (indptr == nullptr || num_tokens < 1 || (k_out == nullptr && v_out == nullptr)) return EKV_ERR_INVALID_ARG;
+  if (!aligned16(k_out) || !aligned16(v_out)) return EKV_ERR_INVALID_ARG;
+  return cuda_status(launch_q4_read(*cache, *seqs, indptr, num_tokens, out_dtype, k_out, v_out,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+EKV_API ekv_status ekv_softmax_decode_mod(const ekv_cache* cache, const ekv_seqs* seqs, const void* q,
+                                          int32_t num_q_heads, int32_t num_q_tokens, float scale,
+                                          const ekv_score_mod* mod, const int32_t* sel, const int32_t* n_sel,
+                                          int32_t cap, float* out, float* lse, void* ws, size_t ws_bytes,
+                                          void* stream) {
+  EKV_TRY(check_cache(cache, true, false));
+  return softmax_mod(*cache, nullptr, seqs, q, num_q_heads, num_q_tokens, scale, mod, sel, n_sel, cap, out, lse, ws,
+                     ws_bytes, stream);
+}
+
+EKV_API ekv_status ekv_softmax_decode_q4(const ekv_cache_q4* cache, const ekv_seqs* seqs, const void* q,
+                                         int32_t num_q_heads, int32_t num_q_tokens, float scale,
+                                         const ekv_score_mod* mod, const int32_t* sel, const int32_t* n_sel,
+                                         int32_t cap, float* out, float* lse, void* ws, size_t ws_bytes,
+                                         void* stream) {
+  EKV_TRY(check_q4(cache));
+  return softmax_mod(q4_shape(cache), cache->pool, seqs, q, num_q_heads, num_q_tokens, scale, mod, sel, n_sel, cap,
+                     out, lse, ws, ws_bytes, stream);
+}
+
+EKV_API size_t ekv_softmax_mod_workspace_bytes(int32_t head_dim, int32_t num_kv_heads, int32_t num_q_heads,
+                                               int32_t num_q_tokens) {
+  if ((head_dim != 64 && head_dim != 128) || num_kv_heads < 1 || num_q_heads < 1 || num_q_tokens < 1) return 0;
+  if (num_q_heads % num_kv_heads != 0 || !pow2_group(num_q_heads / num_kv_heads)) return 0;
+  if (num_q_tokens > kModMaxRows || num_q_heads / num_kv_heads * num_q_tokens > kModMaxRows) return 0;
+  return softmax_mod_ws_bytes(head_dim, num_q_heads / num_kv_heads * num_q_tokens);
 }
 
 EKV_API ekv_status ekv_decode_step(const ekv_cache* cache, const ekv_seqs* seqs,

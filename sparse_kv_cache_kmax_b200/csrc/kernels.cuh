@@ -84,6 +84,22 @@ cudaError_t launch_softmax_decode(const ekv_cache& c, const ekv_seqs& s, const v
                                   float scale, const int32_t* sel, const int32_t* n_sel, int cap,
                                   float* out, float* lse, void* ws, cudaStream_t st);
 
+// Rotated append and 4-bit read-back (rope_append.cu).
+cudaError_t launch_rope_append(const ekv_cache& c, const ekv_seqs& s, const ekv_rope* rope,
+                               const ekv_new_tokens& n, cudaStream_t st);
+cudaError_t launch_rope_append_q4(const ekv_cache_q4& c, const ekv_seqs& s, const ekv_rope* rope,
+                                  const ekv_new_tokens& n, cudaStream_t st);
+cudaError_t launch_q4_read(const ekv_cache_q4& c, const ekv_seqs& s, const int32_t* indptr, int num_tokens,
+                           int out_dtype, void* k_out, void* v_out, cudaStream_t st);
+
+// Softmax decode with capped, biased and masked scores (softmax_mod.cu).
+// pool: the 4-bit pool, or NULL for the bf16 pools of c.
+constexpr int kModMaxRows = 64;  // query rows per KV head: G·T
+size_t softmax_mod_ws_bytes(int d, int rows);
+cudaError_t launch_softmax_mod(const ekv_cache& c, const void* pool, const ekv_seqs& s, const void* q, int Hq, int T,
+                               float scale, const ekv_score_mod* mod, const int32_t* sel, const int32_t* n_sel,
+                               int cap, float* out, float* lse, void* ws, cudaStream_t st);
+
 // Kernels one launch_decode enqueues for these sizes (2: split decode, 1: cluster decode, 3: three-kernel decode).
 int decode_kernel_count(const ekv_cache& c, const ekv_seqs& s, int Hq, int cap, int dense_v);
 

@@ -1,0 +1,978 @@
+// Softmax decode with capped, biased and masked scores over a paged cache held
+// in bf16 or in 4 bits (include/ekv.h: ekv_softmax_decode_mod,
+// ekv_softmax_decode_q4), for the G query heads of a KV head times T query
+// tokens, at most 64 query rows.
+//
+// The work is a list of 16-token tiles: those with a visible token, or those
+// of the selected pages, of every (sequence, KV head) in turn.  One wave of
+// CTAs cuts the whole list into equal runs, whatever the lengths of a ragged
+// batch, so every SM streams the same number of bytes; a CTA walks its run
+// unit by unit.  Within a unit its warps take every NS-th tile through a
+// private ring of bulk copies and keep an online softmax each (running
+// maximum, sum, p·v); at the unit's end they are added in warp order.  A unit
+// cut by a CTA's border leaves partial results, which a second launch adds in
+// CTA order: no atomics, results do not depend on timing.
+//
+// Per tile and warp, with N = 8·NT query rows as the N side of m16n8k16:
+//   Sᵀ[16 tokens × N] = K·Qᵀ          A = K rows,  B = Qᵀ
+//   Oᵀ[d × N]        += Vᵀ·Pᵀ         A = Vᵀ,      B = Pᵀ (8×8 transposes)
+// The query rows sit on the N side because a group has 1 to 16 heads: with
+// them as M, at least half of every product would be padding.  p is split into
+// three bf16 parts (3 × 8 bits: exact), so p·v has fp32's precision although
+// the products run on the bf16 tensor path; that costs 16 more products per
+// tile and stays far below the time the tile's bytes take.
+//
+// The bound is HBM: 512 bytes per bf16 (token, KV head), 136 in 4 bits.
+#include <cuda.h>
+
+#include "q4.cuh"
+
+namespace ekv {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+constexpr int kModCtas = 296;     // two resident CTAs on each of 148 SMs: one wave
+constexpr float kGrow = 8.0f;     // a score may pass the reference maximum by 2^8 before the state is rescaled
+
+struct ModArgs {
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const bf16* q;
+  const int32_t* sel;
+  const int32_t* n_sel;
+  const float* slopes;
+  const int32_t* prefix_lens;
+  const int32_t* starts;
+  const unsigned char* pool;  // 4-bit records
+  float* out;
+  float* lse;
+  float* part;   // [2·CTAs, rows, D] partial p·v: slot 2c the first unit of CTA c, 2c + 1 its last
+  float2* ml;    // [2·CTAs, rows] (maximum, sum) of a partial, in base 2
+  int2* ref;     // [2·CTAs] positions that the bias of a partial is measured from
+  int4* cut;     // [CTAs] the unit that starts in CTA c and is cut: (unit, first slot, pieces, −)
+  float scale2;  // scale·log2(e), the factor of q·k without a cap
+  float capx;    // scale/softcap
+  float cap2;    // softcap·log2(e); 0: no cap
+  int window, batch, Hkv, Hq, G, T, S, num_phys, max_pages, cap, min_tiles;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh(x): for |x| ≤ 1 the fifth convergent of Lambert's continued fraction,
+// x(945 + 105x² + x⁴)/(945 + 420x² + 15x⁴) (off by x¹¹/9.8e6 at most), above
+// it (e^2x − 1)/(e^2x + 1), where nothing cancels.
+__device__ __forceinline__ float tanh_f32(float x) {
+  const float ax = fabsf(x), x2 = x * x;
+  const float e = ex2(fminf(ax, 15.f) * (2.f * kLog2e));
+  const float num = ax <= 1.f ? ax * fmaf(x2, x2 + 105.f, 945.f) : e - 1.f;
+  const float den = ax <= 1.f ? fmaf(x2, fmaf(x2, 15.f, 420.f), 945.f) : e + 1.f;
+  const float t = __fdividef(num, den);
+  return x != x ? x : copysignf(t, x);
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// o += A·(the three parts of p).  The tensor cores drop bits when they add to
+// an accumulator; over thousands of tokens that shrinks it by 1e-5 and more.  So
+// each tile starts from zero, small parts first, and is added with rounding.
+__device__ __forceinline__ void add_product(float (&o)[4], const uint32_t (&af)[4], const uint32_t (&pf)[3][2]) {
+  float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int part = 2; part >= 0; --part) mma_bf16(t, af, pf[part][0], pf[part][1]);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] += t[e];
+}
+
+__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// What one sequence lets its queries see, as tiles: nA from tile a0, then from
+// tile b0 (a prefix, and the window behind it).
+struct Visible {
+  int L, start, prefix, a0, nA, b0, n;
+};
+
+__device__ __forceinline__ Visible visible_tiles(const ModArgs& a, int b) {
+  Visible v;
+  int L = a.seq_lens[b];
+  const int most = a.max_pages * a.S;
+  if (L < 0 || L > most) {
+    raise_flag(EKV_EFLAG_BAD_LEN);
+    L = L < 0 ? 0 : most;
+  }
+  v.L = L;
+  v.start = a.starts ? max(0, a.starts[b]) : 0;
+  v.prefix = a.prefix_lens ? max(0, min(a.prefix_lens[b], L)) : 0;
+  v.a0 = v.nA = v.b0 = v.n = 0;
+  if (v.start >= L) return v;
+  int lo = v.start;
+  if (a.window > 0) lo = max(lo, L - a.T - a.window + 1);
+  const int t_end = (L + kTile - 1) / kTile;
+  v.b0 = lo / kTile;
+  if (v.prefix > v.start && lo > v.start) {
+    v.a0 = v.start / kTile;
+    v.nA = min((v.prefix + kTile - 1) / kTile, v.b0) - v.a0;
+    if (v.nA < 0) v.nA = 0;
+  }
+  v.n = v.nA + t_end - v.b0;
+  return v;
+}
+
+// Tiles of one entry of the work list's outer level: a unit when pages are
+// selected, else a sequence's count per KV head.  At least one: a unit that
+// sees nothing gets one empty tile, which writes its rows.
+__device__ __forceinline__ int group_tiles(const ModArgs& a, int grp) {
+  if (a.sel == nullptr) return max(1, visible_tiles(a, grp).n);
+  return max(1, max(0, min(a.n_sel[grp], a.cap)) * (a.S / kTile));
+}
+
+// The part of a unit that this CTA works on: tiles t0 .. t1−1 of n.
+struct Segment {
+  Visible vis;
+  int unit, b, h, t0, t1, n;
+};
+
+// The physical place of a tile (row of the pools, or record of the 4-bit pool)
+// and the position of its first token; −1: nothing there to see.
+struct Tile {
+  int at, j0;
+};
+
+__device__ __forceinline__ Tile resolve_tile(const ModArgs& a, const Segment& s, int t) {
+  Tile r{-1, 0};
+  if (t >= s.t1 || s.vis.n == 0) return r;
+  const int tpp = a.S / kTile;
+  int lp, part;
+  if (a.sel == nullptr) {
+    const int tile = t < s.vis.nA ? s.vis.a0 + t : s.vis.b0 + t - s.vis.nA;
+    lp = tile / tpp;
+    part = tile - lp * tpp;
+  } else {
+    const int slot = t / tpp;
+    part = t - slot * tpp;
+    if (slot >= max(0, min(a.n_sel[s.unit], a.cap))) return r;  // the empty unit's tile
+    lp = a.sel[static_cast<size_t>(s.unit) * a.cap + slot];
+    if (lp < 0 || lp >= (s.vis.L + a.S - 1) / a.S) {
+      raise_flag(EKV_EFLAG_BAD_SEL);
+      return r;
+    }
+  }
+  r.j0 = lp * a.S + part * kTile;
+  if (a.sel != nullptr) {  // a page may hold no visible tile
+    const int tile = r.j0 / kTile, k = tile - s.vis.b0;
+    const bool in_b = k >= 0 && r.j0 < s.vis.L;
+    const bool in_a = tile >= s.vis.a0 && tile < s.vis.a0 + s.vis.nA;
+    if (!in_a && !in_b) return r;
+  }
+  const int phys = a.page_table[static_cast<size_t>(s.b) * a.max_pages + lp];
+  if (!phys_ok(phys, a.num_phys)) return r;
+  r.at = (phys * a.Hkv + s.h) * tpp + part;
+  return r;
+}
+
+// Position of a segment's first (last) tile, whether or not it can be read.
+__device__ __forceinline__ int tile_position(const ModArgs& a, const Segment& s, int t) {
+  const int tpp = a.S / kTile;
+  if (s.vis.n == 0) return 0;
+  if (a.sel == nullptr) return (t < s.vis.nA ? s.vis.a0 + t : s.vis.b0 + t - s.vis.nA) * kTile;
+  const int slot = t / tpp;
+  if (slot >= max(0, min(a.n_sel[s.unit], a.cap))) return 0;
+  const int lp = a.sel[static_cast<size_t>(s.unit) * a.cap + slot];
+  return lp < 0 || lp >= a.max_pages ? 0 : lp * a.S + (t - slot * tpp) * kTile;
+}
+
+// The distance that the bias of a piece is measured from, so that far tokens
+// keep their differences in fp32: the nearest one for a falling bias, the
+// farthest for a rising one.  Any value is right; this one is precise.
+__device__ __forceinline__ int ref_distance(float slope, int i, int2 ref) {
+  return slope >= 0.f ? max(0, i - ref.y) : abs(i - ref.x);
+}
+
+template <int D, bool Q4>
+struct Shape {
+  static constexpr int NW = 4;                                   // warps of a CTA
+  static constexpr int tile_bytes = Q4 ? q4_record_bytes(D) : 2 * kTile * D * 2;
+  static constexpr int slot_bytes = (tile_bytes + 127) / 128 * 128;
+  static constexpr int threads = 32 * NW;
+};
+
+template <int D, int NT, int R, bool Q4>
+constexpr int mod_stages() {
+  // as many copies in flight as two CTAs' shared memory holds beside the merge buffer
+  constexpr int merge = (Shape<D, Q4>::NW * 8 * NT) * (D + 4) * 4;
+  constexpr int streams = Shape<D, Q4>::NW / R;
+  constexpr int room = 112 * 1024 - merge;
+  constexpr int n = room / (streams * Shape<D, Q4>::slot_bytes);
+  return n > 6 ? 6 : n;
+}
+
+template <int D, int NT, int R, bool Q4>
+constexpr size_t mod_smem() {
+  return 1024 + static_cast<size_t>(Shape<D, Q4>::NW / R) * mod_stages<D, NT, R, Q4>() * Shape<D, Q4>::slot_bytes +
+         static_cast<size_t>(Shape<D, Q4>::NW * 8 * NT) * (D + 4) * 4;
+}
+
+// NT: 8-row groups of query rows per warp; R: warps that share a tile stream,
+// each with its own rows (8·NT·R ≥ G·T).
+template <int D, int NT, int R, bool Q4>
+__global__ void __launch_bounds__(Shape<D, Q4>::threads, 2)
+    mod_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, ModArgs a) {
+  using Sh = Shape<D, Q4>;
+  constexpr int NW = Sh::NW, NS = NW / R, ST = mod_stages<D, NT, R, Q4>(), KS = D / 16, MT = D / 16, PITCH = D + 4;
+  static_assert(ST >= 2 && NW % R == 0, "ring too small");
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ uint64_t bars[NS * ST];
+  __shared__ float s_m[NW][8 * NT], s_l[NW][8 * NT], s_c[NW][8 * NT];
+  __shared__ int scan_s[33];
+  __shared__ long long s_at[3];  // group, its first tile, total
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
+  const int stream = warp / R, rg = warp - stream * R;
+  // the ring starts on a 1024-byte boundary: the 128-byte swizzle repeats every 8 rows
+  unsigned char* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  float* red = reinterpret_cast<float*>(ring + NS * ST * Sh::slot_bytes);
+  if (tid < NS * ST) {
+    mbar_init(&bars[tid], 1);
+    fence_mbar_init();
+  }
+  grid_dep_enter();
+
+  // this CTA's run of the work list
+  const int mult = a.sel ? 1 : a.Hkv, groups = a.sel ? a.batch * a.Hkv : a.batch;
+  long long total = 0;
+  for (int c0 = 0; c0 < groups; c0 += Sh::threads) {
+    int sum;
+    block_exclusive_scan(c0 + tid < groups ? group_tiles(a, c0 + tid) * mult : 0, scan_s, &sum);
+    total += sum;
+    __syncthreads();
+  }
+  long long per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < a.min_tiles) per = a.min_tiles;
+  long long pos = per * blockIdx.x;
+  const long long end = pos + per < total ? pos + per : total;
+  if (tid == 0) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+  if (pos >= total) return;
+  long long before = 0;
+  for (int c0 = 0; c0 < groups; c0 += Sh::threads) {
+    int sum;
+    const int mine = c0 + tid < groups ? group_tiles(a, c0 + tid) * mult : 0;
+    const int ex = block_exclusive_scan(mine, scan_s, &sum);
+    if (before + ex <= pos && pos < before + ex + mine) {
+      s_at[0] = c0 + tid;
+      s_at[1] = before + ex;
+    }
+    before += sum;
+    __syncthreads();
+    if (before > pos) break;
+  }
+  int grp = static_cast<int>(s_at[0]);
+  long long grp_at = s_at[1];
+
+  auto load_group = [&](Segment& s) {  // the sequence (and unit) of grp
+    s.b = a.sel ? grp / a.Hkv : grp;
+    s.vis = visible_tiles(a, s.b);
+    s.n = a.sel ? max(1, max(0, min(a.n_sel[grp], a.cap)) * (a.S / kTile)) : max(1, s.vis.n);
+  };
+  auto place = [&](Segment& s) {  // the unit at pos
+    const int off = static_cast<int>(pos - grp_at), hh = off / s.n;
+    s.h = a.sel ? grp % a.Hkv : hh;
+    s.unit = s.b * a.Hkv + s.h;
+    s.t0 = off - hh * s.n;
+    const long long left = end - pos;
+    s.t1 = left < s.n - s.t0 ? s.t0 + static_cast<int>(left) : s.n;
+  };
+
+  unsigned char* my_ring = ring + stream * ST * Sh::slot_bytes;
+  uint64_t* my_bar = bars + stream * ST;
+  int it = 0;  // tiles this stream has consumed: ring position and parity
+  Tile cur, nxt;
+  auto issue = [&](Tile src, int n) {  // lane 0 of the stream's first warp: tile src into ring position n
+    const int sl = n % ST;
+    unsigned char* dst = my_ring + sl * Sh::slot_bytes;
+    if (src.at < 0) {
+      mbar_arrive(&my_bar[sl]);
+      return;
+    }
+    mbar_arrive_expect_tx(&my_bar[sl], Sh::tile_bytes);
+    if constexpr (Q4) {
+      bulk_g2s(dst, a.pool + static_cast<size_t>(src.at) * Sh::tile_bytes, Sh::tile_bytes, &my_bar[sl]);
+    } else {
+#pragma unroll
+      for (int half = 0; half < D / 64; ++half) {
+        tma_2d(dst + half * kTile * 128, &kmap, half * 64, src.at * kTile, &my_bar[sl]);
+        tma_2d(dst + (D / 64 + half) * kTile * 128, &vmap, half * 64, src.at * kTile, &my_bar[sl]);
+      }
+    }
+  };
+  auto stream_tiles = [&](const Segment& s) {
+    const int n = s.t1 - s.t0 - stream;
+    return n > 0 ? (n + NS - 1) / NS : 0;
+  };
+  auto lookup = [&](const Segment& s, int batch32) {
+    return resolve_tile(a, s, s.t0 + stream + NS * (32 * batch32 + lane));
+  };
+  auto pick = [&](const Tile& x, int k) {
+    return Tile{__shfl_sync(0xffffffffu, x.at, k & 31), __shfl_sync(0xffffffffu, x.j0, k & 31)};
+  };
+  auto prologue = [&](const Segment& s) {
+    const int nk = stream_tiles(s);
+    cur = lookup(s, 0);
+    nxt = lookup(s, 1);
+#pragma unroll
+    for (int k = 0; k < ST; ++k) {
+      const Tile x = pick(cur, k);
+      if (lane == 0 && rg == 0 && k < nk) issue(x, it + k);
+    }
+  };
+  auto stream_sync = [&]() {
+    if constexpr (R == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + stream), "r"(32 * R) : "memory");
+  };
+
+  Segment seg;
+  load_group(seg);
+  place(seg);
+  __syncthreads();  // barriers initialised
+  prologue(seg);
+  const int rows = a.G * a.T;
+  bool first_segment = true;
+
+  for (;;) {
+    // ---- the unit's queries
+    int qi[NT][2];       // positions of this lane's columns (rows 2·t4, 2·t4 + 1 of each group of 8)
+    float slope2[NT][2];
+    int2 ref = make_int2(0, 0);
+    if (a.slopes) ref = make_int2(tile_position(a, seg, seg.t0), tile_position(a, seg, seg.t1 - 1) + kTile - 1);
+    int dist0[NT][2];
+    uint32_t qf[KS][NT][2];
+    float qsum[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = (rg * NT + nt) * 8 + 2 * t4 + e, rr = row < rows ? row : 0, t = rr / a.G;
+        qi[nt][e] = seg.vis.L - a.T + t;
+        slope2[nt][e] = 0.f;
+        dist0[nt][e] = 0;
+        if (a.slopes) {
+          const float sl = a.slopes[seg.h * a.G + rr - t * a.G];
+          slope2[nt][e] = sl * kLog2e;
+          dist0[nt][e] = ref_distance(sl, qi[nt][e], ref);
+        }
+      }
+      const int row = (rg * NT + nt) * 8 + g, rr = row < rows ? row : 0, t = rr / a.G;
+      const bf16* qp = a.q + ((static_cast<size_t>(seg.b) * a.T + t) * a.Hq + seg.h * a.G + rr - t * a.G) * D;
+      float sum = 0.f;
+      if constexpr (!Q4) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          qf[ks][nt][0] = *reinterpret_cast<const uint32_t*>(qp + 16 * ks + 2 * t4);
+          qf[ks][nt][1] = *reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8 + 2 * t4);
+        }
+      } else {
+        // the k order of the codes: word w of lane t4's share (D/4 numbers from
+        // D/4·t4) gives the pairs (8w + i, 8w + i + 4)
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          const uint4 x = *reinterpret_cast<const uint4*>(qp + D / 4 * t4 + 8 * w);
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = xs[i >> 1], hi = xs[2 + (i >> 1)];
+            qf[2 * w + (i >> 1)][nt][i & 1] = __byte_perm(lo, hi, (i & 1) ? 0x7632 : 0x5410);
+            sum += bf16_lo(xs[i]) + bf16_hi(xs[i]);
+          }
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      }
+      qsum[nt][0] = __shfl_sync(0xffffffffu, sum, 8 * t4);
+      qsum[nt][1] = __shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
+    }
+
+    float o[MT][NT][4], m_sub[NT][2], m_lim[NT][2], l[NT][2], corr[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < MT; ++j) o[j][nt][0] = o[j][nt][1] = o[j][nt][2] = o[j][nt][3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m_sub[nt][e] = 0.f;         // subtracted from scores: the reference maximum, 0 while there is none
+        m_lim[nt][e] = -INFINITY;   // a score above it moves the reference
+        l[nt][e] = corr[nt][e] = 0.f;
+      }
+    }
+
+    // ---- the tiles
+    const int nk = stream_tiles(seg);
+    const int i_first = seg.vis.L - a.T, i_last = seg.vis.L - 1;
+    for (int k = 0; k < nk; ++k, ++it) {
+      if (k > 0 && (k & 31) == 0) {
+        cur = nxt;
+        nxt = lookup(seg, (k >> 5) + 1);
+      }
+      const Tile tl = pick(cur, k);
+      const int sl = it % ST;
+      const unsigned int parity = static_cast<unsigned int>(it / ST) & 1u;
+      if (!mbar_wait(&my_bar[sl], parity)) mbar_wait(&my_bar[sl], parity);
+      if (tl.at >= 0) {
+        unsigned char* buf = my_ring + sl * Sh::slot_bytes;
+        // scores
+        float z[NT][4];
+        float vs[2], vmid[2];  // 4 bits: V's step and the value of code 8, of tokens g and g + 8
+        if constexpr (!Q4) {
+          float z2[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[nt][e] = z2[nt][e] = 0.f;
+          const uint32_t kbase = smem_addr(buf);
+          const int tok = lane & 15, ch = lane >> 4;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const int c = 2 * ks + ch;
+            uint32_t af[4];
+            ldsm_x4(kbase + (c >> 3) * (kTile * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4), af);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_bf16(ks & 1 ? z2[nt] : z[nt], af, qf[ks][nt][0], qf[ks][nt][1]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[nt][e] += z2[nt][e];
+        } else {
+          float z2[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[nt][e] = z2[nt][e] = 0.f;
+          uint32_t w0[D / 32], w1[D / 32];
+          const unsigned char* k0 = buf + g * (D / 2) + t4 * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(k0), y = *reinterpret_cast<const uint4*>(k0 + 8 * (D / 2));
+            w0[0] = x.x; w0[1] = x.y; w0[2] = x.z; w0[3] = x.w;
+            w1[0] = y.x; w1[1] = y.y; w1[2] = y.z; w1[3] = y.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(k0), y = *reinterpret_cast<const uint2*>(k0 + 8 * (D / 2));
+            w0[0] = x.x; w0[1] = x.y;
+            w1[0] = y.x; w1[1] = y.y;
+          }
+          const uint32_t* pairs = reinterpret_cast<const uint32_t*>(buf + 16 * D);
+          const uint32_t ka = pairs[g], kb = pairs[g + 8], va = pairs[16 + g], vb = pairs[24 + g];
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const uint32_t af[4] = {q4_pair(w0[w], i), q4_pair(w1[w], i), q4_pair(w0[w], i + 1), q4_pair(w1[w], i + 1)};
+              const int ks = 2 * w + (i >> 1);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_bf16(ks & 1 ? z2[nt] : z[nt], af, qf[ks][nt][0], qf[ks][nt][1]);
+            }
+          const float ks0 = bf16_lo(ka), ks1 = bf16_lo(kb);
+          const float km0 = fmaf(8.f, ks0, bf16_hi(ka)), km1 = fmaf(8.f, ks1, bf16_hi(kb));
+          vs[0] = bf16_lo(va);
+          vs[1] = bf16_lo(vb);
+          vmid[0] = fmaf(8.f, vs[0], bf16_hi(va));
+          vmid[1] = fmaf(8.f, vs[1], bf16_hi(vb));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              z[nt][e] = fmaf(ks0, z[nt][e] + z2[nt][e], km0 * qsum[nt][e]);
+              z[nt][2 + e] = fmaf(ks1, z[nt][2 + e] + z2[nt][2 + e], km1 * qsum[nt][e]);
+            }
+        }
+        // cap, bias
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            z[nt][e] = a.cap2 != 0.f ? a.cap2 * tanh_f32(z[nt][e] * a.capx) : z[nt][e] * a.scale2;
+        if (a.slopes) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = tl.j0 + g + (e >> 1) * 8;
+              z[nt][e] = fmaf(-slope2[nt][e & 1], static_cast<float>(abs(qi[nt][e & 1] - j) - dist0[nt][e & 1]), z[nt][e]);
+            }
+        }
+        // masks: only tiles that not every row sees whole
+        const bool whole = tl.j0 >= seg.vis.start &&
+                           (tl.j0 + kTile <= seg.vis.prefix ||
+                            (tl.j0 + kTile - 1 <= i_first && (a.window <= 0 || i_last - tl.j0 < a.window)));
+        uint32_t apart = 0;  // bf16: tokens that some rows see and others do not, with a V that is not finite
+        if (!whole) {
+          auto sees = [&](int i, int j) {
+            return j >= seg.vis.start && i >= 0 && j < seg.vis.L &&
+                   (j < seg.vis.prefix || (j <= i && (a.window <= 0 || i - j < a.window)));
+          };
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!sees(qi[nt][e & 1], tl.j0 + g + (e >> 1) * 8)) z[nt][e] = -INFINITY;
+          if constexpr (!Q4) {
+            // 0·V must not turn a masked NaN into the sum: rows of V that nobody
+            // sees are zeroed; a row only some see is set apart if it has one
+            bool any = false, all = true;
+            if (lane < kTile)
+              for (int t = 0; t < a.T; ++t) {
+                const bool v = sees(i_first + t, tl.j0 + lane);
+                any |= v;
+                all &= v;
+              }
+            const uint32_t seen = __ballot_sync(0xffffffffu, any && lane < kTile);
+            uint32_t some = seen & ~__ballot_sync(0xffffffffu, all && lane < kTile);
+            unsigned char* vt = buf + D / 64 * kTile * 128;
+            for (uint32_t rest = ~seen & 0xffffu; rest; rest &= rest - 1) {
+              const int tok = __ffs(rest) - 1;
+              if (lane < D / 8)
+                *reinterpret_cast<uint4*>(vt + (lane >> 3) * (kTile * 128) + tok * 128 + (lane & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            for (; some; some &= some - 1) {
+              const int tok = __ffs(some) - 1;
+              bool bad = false;
+              if (lane < D / 8) {
+                const uint4 x = *reinterpret_cast<const uint4*>(vt + (lane >> 3) * (kTile * 128) + tok * 128 + (lane & 7) * 16);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  bad |= (xs[i] & 0x7f80u) == 0x7f80u || (xs[i] & 0x7f800000u) == 0x7f800000u;
+              }
+              if (__any_sync(0xffffffffu, bad)) apart |= 1u << tok;
+            }
+            __syncwarp();
+          }
+        }
+        // a score far above the reference: new maxima, and the state follows
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) grow |= z[nt][e] > m_lim[nt][e & 1];
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(z[nt][e], z[nt][2 + e]);
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+              const float old = m_lim[nt][e] - kGrow;  // −inf at first
+              if (top > old) {
+                const float f = ex2(old - top);
+                m_sub[nt][e] = top;
+                m_lim[nt][e] = top + kGrow;
+                l[nt][e] *= f;
+                corr[nt][e] *= f;
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                  o[j][nt][e] *= f;
+                  o[j][nt][2 + e] *= f;
+                }
+              }
+            }
+        }
+        // weights, and their three bf16 parts as B fragments
+        uint32_t pf[NT][3][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[e] = ex2(z[nt][e] - m_sub[nt][e & 1]);
+            l[nt][e & 1] += p[e];
+          }
+          if constexpr (!Q4) {
+            if (apart) {
+              // tokens set apart, by hand: only rows that see them, p > 0
+              const unsigned char* vt = buf + D / 64 * kTile * 128;
+              for (uint32_t rest = apart; rest; rest &= rest - 1) {
+                const int tok = __ffs(rest) - 1, from = (tok & 7) * 4 + t4;
+                const float pa = __shfl_sync(0xffffffffu, tok < 8 ? p[0] : p[2], from);
+                const float pb = __shfl_sync(0xffffffffu, tok < 8 ? p[1] : p[3], from);
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int col = 16 * j + 8 * e + g, c = (col & 63) >> 3;
+                    const float v = __bfloat162float(*reinterpret_cast<const bf16*>(
+                        vt + (col >> 6) * (kTile * 128) + tok * 128 + ((c ^ (tok & 7)) << 4) + (col & 7) * 2));
+                    if (pa > 0.f) o[j][nt][2 * e] = fmaf(pa, v, o[j][nt][2 * e]);
+                    if (pb > 0.f) o[j][nt][2 * e + 1] = fmaf(pb, v, o[j][nt][2 * e + 1]);
+                  }
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              // a masked token's pair may hold anything
+              const bool on = whole || p[e] > 0.f;
+              if (on) corr[nt][e & 1] = fmaf(p[e], vmid[e >> 1], corr[nt][e & 1]);
+              p[e] = on ? p[e] * vs[e >> 1] : 0.f;
+            }
+          }
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            pf[nt][part][0] = transpose8x8(__byte_perm(__float_as_uint(p[0]), __float_as_uint(p[1]), 0x7632));
+            pf[nt][part][1] = transpose8x8(__byte_perm(__float_as_uint(p[2]), __float_as_uint(p[3]), 0x7632));
+            if (part < 2) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) p[e] -= __uint_as_float(__float_as_uint(p[e]) & 0xffff0000u);
+            }
+          }
+        }
+        if constexpr (!Q4) {
+          if (apart) {
+            stream_sync();  // the warps that share the tile have all read the rows
+            unsigned char* vt = buf + D / 64 * kTile * 128;
+            for (uint32_t rest = apart; rest; rest &= rest - 1) {
+              const int tok = __ffs(rest) - 1;
+              if (lane < D / 8)
+                *reinterpret_cast<uint4*>(vt + (lane >> 3) * (kTile * 128) + tok * 128 + (lane & 7) * 16) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            }
+            __syncwarp();
+          }
+        }
+        // p·v
+        if constexpr (!Q4) {
+          const uint32_t vbase = smem_addr(buf) + D / 64 * kTile * 128;
+          const int tok = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            const int c = 2 * j + ch;
+            uint32_t af[4];
+            ldsm_x4_trans(vbase + (c >> 3) * (kTile * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4), af);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) add_product(o[j][nt], af, pf[nt]);
+          }
+        } else {
+          // lane (g, t4): tokens 2·t4, 2·t4 + 1 (+ 8), numbers D/8·g … of each;
+          // the byte interleave pairs the two tokens' codes of one number
+          constexpr int VW = D / 64;  // words per lane and token
+          uint32_t wv[4][VW];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const unsigned char* src = buf + 8 * D + (2 * t4 + (x & 1) + (x >> 1) * 8) * (D / 2) + g * (D / 16);
+            if constexpr (VW == 2) {
+              const uint2 y = *reinterpret_cast<const uint2*>(src);
+              wv[x][0] = y.x;
+              wv[x][1] = y.y;
+            } else {
+              wv[x][0] = *reinterpret_cast<const uint32_t*>(src);
+            }
+          }
+          uint32_t un[2][2 * VW];  // [tokens, tokens + 8][four numbers each]
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+              un[hf][2 * w] = __byte_perm(wv[2 * hf][w], wv[2 * hf + 1][w], 0x5410);
+              un[hf][2 * w + 1] = __byte_perm(wv[2 * hf][w], wv[2 * hf + 1][w], 0x7632);
+            }
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            // m rows g: number j of the lane's share; rows g + 8: number MT + j
+            const uint32_t af[4] = {q4_pair(un[0][j / 4], j & 3), q4_pair(un[0][MT / 4 + j / 4], j & 3),
+                                    q4_pair(un[1][j / 4], j & 3), q4_pair(un[1][MT / 4 + j / 4], j & 3)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) add_product(o[j][nt], af, pf[nt]);
+          }
+        }
+      }
+      // the slot is free: the next copy into it
+      stream_sync();
+      const int ahead = k + ST;
+      const Tile x = pick((ahead >> 5) == (k >> 5) ? cur : nxt, ahead);
+      if (lane == 0 && rg == 0 && ahead < nk) {
+        fence_proxy_async_shared();  // the slot's reads come before the copies that refill it
+        issue(x, it + ST);
+      }
+    }
+
+    // ---- the next unit's copies start before this one's warps are added up
+    const Segment done = seg;
+    pos += seg.t1 - seg.t0;
+    const bool more = pos < end;
+    if (more) {
+      if (pos >= grp_at + static_cast<long long>(seg.n) * mult) {
+        grp_at += static_cast<long long>(seg.n) * mult;
+        ++grp;
+        load_group(seg);
+      }
+      place(seg);
+      prologue(seg);
+    }
+
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) {
+          l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], sh);
+          if constexpr (Q4) corr[nt][e] += __shfl_xor_sync(0xffffffffu, corr[nt][e], sh);
+        }
+        if (g == 0) {
+          s_m[warp][nt * 8 + 2 * t4 + e] = m_lim[nt][e] - kGrow;
+          s_l[warp][nt * 8 + 2 * t4 + e] = l[nt][e];
+          s_c[warp][nt * 8 + 2 * t4 + e] = corr[nt][e];
+        }
+      }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = nt * 8 + 2 * t4 + e;
+        float top = -INFINITY;
+#pragma unroll
+        for (int s = 0; s < NS; ++s) top = fmaxf(top, s_m[s * R + rg][row]);
+        const float mine = s_m[warp][row], f = mine > -INFINITY ? ex2(mine - top) : 0.f;
+        float* to = red + (warp * 8 * NT + row) * PITCH;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          to[Q4 ? D / 8 * g + j : 16 * j + g] = o[j][nt][e] * f;
+          to[Q4 ? D / 8 * g + MT + j : 16 * j + 8 + g] = o[j][nt][2 + e] * f;
+        }
+      }
+    __syncthreads();
+    const bool entire = done.t0 == 0 && done.t1 == done.n;
+    const int slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
+    for (int i = tid; i < rows * (D / 4); i += Sh::threads) {
+      const int row = i / (D / 4), c = (i - row * (D / 4)) * 4, r = row / (8 * NT), in = row - r * (8 * NT);
+      float top = -INFINITY;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) top = fmaxf(top, s_m[s * R + r][in]);
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+      float den = 0.f, cc = 0.f;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int w = s * R + r;
+        const float4 x = *reinterpret_cast<const float4*>(red + (w * 8 * NT + in) * PITCH + c);
+        const float f = s_m[w][in] > -INFINITY ? ex2(s_m[w][in] - top) : 0.f;
+        sum.x += x.x;
+        sum.y += x.y;
+        sum.z += x.z;
+        sum.w += x.w;
+        den = fmaf(s_l[w][in], f, den);
+        cc = fmaf(s_c[w][in], f, cc);
+      }
+      if constexpr (Q4) {
+        sum.x += cc;
+        sum.y += cc;
+        sum.z += cc;
+        sum.w += cc;
+      }
+      if (entire) {
+        const int t = row / a.G, hq = done.h * a.G + row - t * a.G;
+        const size_t orow = (static_cast<size_t>(done.b) * a.T + t) * a.Hq + hq;
+        const bool none = top == -INFINITY && den == den;  // no visible token with a score above −inf
+        const float by = none ? 0.f : 1.f / den;
+        *reinterpret_cast<float4*>(a.out + orow * D + c) =
+            none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(sum.x * by, sum.y * by, sum.z * by, sum.w * by);
+        if (c == 0 && a.lse) {
+          float lse = none ? -INFINITY : (top + log2f(den)) * kLn2;
+          if (a.slopes && !none) {
+            const float sl = a.slopes[hq];
+            lse -= sl * static_cast<float>(ref_distance(sl, done.vis.L - a.T + t, ref));
+          }
+          a.lse[orow] = lse;
+        }
+      } else {
+        *reinterpret_cast<float4*>(a.part + (static_cast<size_t>(slot) * rows + row) * D + c) = sum;
+        if (c == 0) a.ml[static_cast<size_t>(slot) * rows + row] = make_float2(top, den);
+      }
+    }
+    if (!entire && tid == 0) {
+      a.ref[slot] = ref;
+      if (done.t0 == 0) {  // the unit's first piece: CTAs that hold the others follow
+        const long long last = pos - (done.t1 - done.t0) + done.n - 1;
+        a.cut[blockIdx.x] = make_int4(done.unit, slot, static_cast<int>(last / per) - static_cast<int>(blockIdx.x) + 1, 0);
+      }
+    }
+    if (!more) return;
+    first_segment = false;
+    __syncthreads();
+  }
+}
+
+// grid (CTAs of mod_kernel, rows), D threads × 4 slices of the pieces: adds the
+// pieces of the unit that CTA x cut, in CTA order.
+template <int D>
+__global__ void __launch_bounds__(4 * D) mod_combine_kernel(ModArgs a) {
+  grid_dep_enter();
+  const int4 cut = a.cut[blockIdx.x];
+  if (cut.z == 0) return;
+  __shared__ float s_num[4][D], s_den[4];
+  const int rows = a.G * a.T, row = blockIdx.y, c = threadIdx.x % D, sl = threadIdx.x / D;
+  const int b = cut.x / a.Hkv, h = cut.x - b * a.Hkv, t = row / a.G, hq = h * a.G + row - t * a.G;
+  const int cta = blockIdx.x, n = cut.z;
+  auto slot = [&](int p) { return static_cast<size_t>(p == 0 ? cut.y : 2 * (cta + p)); };
+  float slope = 0.f;
+  int i = 0;
+  if (a.slopes) {
+    slope = a.slopes[hq];
+    int L = a.seq_lens[b];
+    const int most = a.max_pages * a.S;
+    L = L < 0 ? 0 : (L > most ? most : L);
+    i = L - a.T + t;
+  }
+  // the pieces' biases are measured from distances of their own: all to the
+  // last piece's (the nearest tokens), or the first's for a rising bias
+  const int base = a.slopes ? ref_distance(slope, i, a.ref[slot(slope >= 0.f ? n - 1 : 0)]) : 0;
+  auto top_of = [&](int p) {
+    const float m = a.ml[slot(p) * rows + row].x;
+    return a.slopes ? m - slope * kLog2e * static_cast<float>(ref_distance(slope, i, a.ref[slot(p)]) - base) : m;
+  };
+  float top = -INFINITY;
+  for (int p = threadIdx.x & 31; p < n; p += 32) top = fmaxf(top, top_of(p));
+  top = warp_max(top);
+  float num = 0.f, den = 0.f;
+#pragma unroll 4
+  for (int p = sl; p < n; p += 4) {
+    const float m = top_of(p), f = m > -INFINITY ? ex2(m - top) : 0.f;
+    num = fmaf(a.part[(slot(p) * rows + row) * D + c], f, num);
+    den = fmaf(a.ml[slot(p) * rows + row].y, f, den);
+  }
+  s_num[sl][c] = num;
+  if (c == 0) s_den[sl] = den;
+  __syncthreads();
+  if (sl != 0) return;
+  num = s_num[0][c] + s_num[1][c] + s_num[2][c] + s_num[3][c];
+  den = s_den[0] + s_den[1] + s_den[2] + s_den[3];
+  const size_t orow = (static_cast<size_t>(b) * a.T + t) * a.Hq + hq;
+  const bool none = top == -INFINITY && den == den;
+  a.out[orow * D + c] = none ? 0.f : num / den;
+  if (c == 0 && a.lse)
+    a.lse[orow] = none ? -INFINITY : (top + log2f(den)) * kLn2 - slope * static_cast<float>(base);
+}
+
+// Two-dimensional view [rows, d] of a pool, copied 16 rows × 64 columns at a
+// time with the 128-byte swizzle, which keeps the fragment loads of both
+// products free of bank conflicts.
+cudaError_t pool_map(CUtensorMap* map, void* pool, size_t rows, int d) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static Encode encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r);
+    return e == cudaSuccess && r == cudaDriverEntryPointSuccess ? reinterpret_cast<Encode>(f) : nullptr;
+  }();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(d), rows}, stride[1] = {static_cast<cuuint64_t>(d) * 2};
+  const cuuint32_t box[2] = {64, kTile}, one[2] = {1, 1};
+  const CUresult r =
+      encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pool, dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+inline size_t al256(size_t x) { return (x + 255) / 256 * 256; }
+
+template <int D, int NT, int R, bool Q4>
+cudaError_t run_mod(const ModArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+  constexpr size_t smem = mod_smem<D, NT, R, Q4>();
+  cudaError_t e = cudaFuncSetAttribute(mod_kernel<D, NT, R, Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int ctas = min(kModCtas, 2 * sm_count());
+  e = launch_k(mod_kernel<D, NT, R, Q4>, dim3(static_cast<unsigned>(ctas)), Shape<D, Q4>::threads, smem, st, km, vm, a);
+  if (e != cudaSuccess) return e;
+  return launch_k(mod_combine_kernel<D>, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(a.G * a.T)), 4 * D, 0,
+                  st, a);
+}
+
+template <int D, bool Q4>
+cudaError_t dispatch_rows(const ModArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
+  const int rows = a.G * a.T;
+  if (rows <= 8) return run_mod<D, 1, 1, Q4>(a, km, vm, st);
+  if (rows <= 16) return run_mod<D, 2, 1, Q4>(a, km, vm, st);
+  if (rows <= 32) return run_mod<D, 2, 2, Q4>(a, km, vm, st);
+  return run_mod<D, 2, 4, Q4>(a, km, vm, st);
+}
+
+}  // namespace
+
+size_t softmax_mod_ws_bytes(int d, int rows) {
+  const size_t slots = 2 * static_cast<size_t>(kModCtas);
+  return al256(slots * rows * d * sizeof(float)) + al256(slots * rows * sizeof(float2)) + al256(slots * sizeof(int2)) +
+         al256(kModCtas * sizeof(int4));
+}
+
+// pool: the 4-bit pool, or NULL for the bf16 pools of c.
+cudaError_t launch_softmax_mod(const ekv_cache& c, const void* pool, const ekv_seqs& s, const void* q, int Hq, int T,
+                               float scale, const ekv_score_mod* mod, const int32_t* sel, const int32_t* n_sel,
+                               int cap, float* out, float* lse, void* ws, cudaStream_t st) {
+  ModArgs a{};
+  a.page_table = s.page_table;
+  a.seq_lens = s.seq_lens;
+  a.q = static_cast<const bf16*>(q);
+  a.sel = sel;
+  a.n_sel = n_sel;
+  a.pool = static_cast<const unsigned char*>(pool);
+  a.out = out;
+  a.lse = lse;
+  a.batch = s.batch;
+  a.Hkv = c.num_kv_heads;
+  a.Hq = Hq;
+  a.G = Hq / c.num_kv_heads;
+  a.T = T;
+  a.S = c.page_size;
+  a.num_phys = c.num_phys_pages;
+  a.max_pages = s.max_pages;
+  a.cap = cap;
+  a.min_tiles = 8;
+  a.scale2 = scale * kLog2e;
+  if (mod != nullptr) {
+    a.slopes = mod->slopes;
+    a.prefix_lens = mod->prefix_lens;
+    a.starts = mod->starts;
+    a.window = mod->window;
+    if (mod->softcap > 0.f) {
+      a.capx = scale / mod->softcap;
+      a.cap2 = mod->softcap * kLog2e;
+    }
+  }
+  const int d = c.head_dim, rows = a.G * T;
+  const size_t slots = 2 * static_cast<size_t>(kModCtas);
+  char* p = static_cast<char*>(ws);
+  a.part = reinterpret_cast<float*>(p);
+  p += al256(slots * rows * d * sizeof(float));
+  a.ml = reinterpret_cast<float2*>(p);
+  p += al256(slots * rows * sizeof(float2));
+  a.ref = reinterpret_cast<int2*>(p);
+  p += al256(slots * sizeof(int2));
+  a.cut = reinterpret_cast<int4*>(p);
+  CUtensorMap km{}, vm{};
+  if (pool == nullptr) {
+    const size_t pool_rows = static_cast<size_t>(c.num_phys_pages) * c.num_kv_heads * c.page_size;
+    cudaError_t e = pool_map(&km, c.k_pool, pool_rows, d);
+    if (e == cudaSuccess) e = pool_map(&vm, c.v_pool, pool_rows, d);
+    if (e != cudaSuccess) return e;
+    return d == 128 ? dispatch_rows<128, false>(a, km, vm, st) : dispatch_rows<64, false>(a, km, vm, st);
+  }
+  return d == 128 ? dispatch_rows<128, true>(a, km, vm, st) : dispatch_rows<64, true>(a, km, vm, st);
+}
+
+}  // namespace ekv
