@@ -75,21 +75,19 @@ __device__ __forceinline__ float tanh_f32(float x) {
   return x != x ? x : copysignf(t, x);
 }
 
+// As mma_bf16, with fp16 operands.
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-// o += A·(the three parts of p).  The tensor cores drop bits when they add to
-// an accumulator; over thousands of tokens that shrinks it by 1e-5 and more.  So
-// each tile starts from zero, small parts first, and is added with rounding.
-__device__ __forceinline__ void add_product(float (&o)[4], const uint32_t (&af)[4], const uint32_t (&pf)[3][2]) {
-  float t[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int part = 2; part >= 0; --part) mma_bf16(t, af, pf[part][0], pf[part][1]);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] += t[e];
 }
 
 __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
@@ -147,13 +145,15 @@ struct Segment {
 };
 
 // The physical place of a tile (row of the pools, or record of the 4-bit pool)
-// and the position of its first token; −1: nothing there to see.
+// and the position of its first token, a multiple of 16; bit 0 of j0 says that
+// every row sees all of it, so that most tiles need no masks.  at = −1: nothing
+// there to see, and a position that no mask lets through.
 struct Tile {
   int at, j0;
 };
 
 __device__ __forceinline__ Tile resolve_tile(const ModArgs& a, const Segment& s, int t) {
-  Tile r{-1, 0};
+  Tile r{-1, -kTile};
   if (t >= s.t1 || s.vis.n == 0) return r;
   const int tpp = a.S / kTile;
   int lp, part;
@@ -171,16 +171,20 @@ __device__ __forceinline__ Tile resolve_tile(const ModArgs& a, const Segment& s,
       return r;
     }
   }
-  r.j0 = lp * a.S + part * kTile;
+  const int j0 = lp * a.S + part * kTile;
   if (a.sel != nullptr) {  // a page may hold no visible tile
-    const int tile = r.j0 / kTile, k = tile - s.vis.b0;
-    const bool in_b = k >= 0 && r.j0 < s.vis.L;
+    const int tile = j0 / kTile;
+    const bool in_b = tile >= s.vis.b0 && j0 < s.vis.L;
     const bool in_a = tile >= s.vis.a0 && tile < s.vis.a0 + s.vis.nA;
     if (!in_a && !in_b) return r;
   }
   const int phys = a.page_table[static_cast<size_t>(s.b) * a.max_pages + lp];
   if (!phys_ok(phys, a.num_phys)) return r;
   r.at = (phys * a.Hkv + s.h) * tpp + part;
+  const bool whole = j0 >= s.vis.start &&
+                     (j0 + kTile <= s.vis.prefix ||
+                      (j0 + kTile <= s.vis.L - a.T + 1 && (a.window <= 0 || s.vis.L - 1 - j0 < a.window)));
+  r.j0 = j0 | (whole ? 1 : 0);
   return r;
 }
 
@@ -202,37 +206,43 @@ __device__ __forceinline__ int ref_distance(float slope, int i, int2 ref) {
   return slope >= 0.f ? max(0, i - ref.y) : abs(i - ref.x);
 }
 
-template <int D, bool Q4>
+// NT: groups of 8 query rows per warp.  4 bits at NT = 1: eight warps of at most
+// 128 registers and two tiles a step, since turning codes into numbers keeps the
+// issue slots busy and what is done once per step counts (see q4 below); else
+// four warps and one tile, where copies alone bound the step.
+template <int D, int NT, bool Q4>
 struct Shape {
-  static constexpr int NW = 4;                                   // warps of a CTA
+  static constexpr int NW = Q4 && NT == 1 ? 8 : 4;  // warps of a CTA
+  static constexpr int U = Q4 && NT == 1 ? 2 : 1;   // tiles of a step
   static constexpr int tile_bytes = Q4 ? q4_record_bytes(D) : 2 * kTile * D * 2;
-  static constexpr int slot_bytes = (tile_bytes + 127) / 128 * 128;
+  static constexpr int slot_bytes = U * ((tile_bytes + 127) / 128 * 128);
   static constexpr int threads = 32 * NW;
 };
 
 template <int D, int NT, int R, bool Q4>
 constexpr int mod_stages() {
   // as many copies in flight as two CTAs' shared memory holds beside the merge buffer
-  constexpr int merge = (Shape<D, Q4>::NW * 8 * NT) * (D + 4) * 4;
-  constexpr int streams = Shape<D, Q4>::NW / R;
+  using Sh = Shape<D, NT, Q4>;
+  constexpr int merge = (Sh::NW * 8 * NT) * (D + 4) * 4;
   constexpr int room = 112 * 1024 - merge;
-  constexpr int n = room / (streams * Shape<D, Q4>::slot_bytes);
+  constexpr int n = room / (Sh::NW / R * Sh::slot_bytes);
   return n > 6 ? 6 : n;
 }
 
 template <int D, int NT, int R, bool Q4>
 constexpr size_t mod_smem() {
-  return 1024 + static_cast<size_t>(Shape<D, Q4>::NW / R) * mod_stages<D, NT, R, Q4>() * Shape<D, Q4>::slot_bytes +
-         static_cast<size_t>(Shape<D, Q4>::NW * 8 * NT) * (D + 4) * 4;
+  using Sh = Shape<D, NT, Q4>;
+  return 1024 + static_cast<size_t>(Sh::NW / R) * mod_stages<D, NT, R, Q4>() * Sh::slot_bytes +
+         static_cast<size_t>(Sh::NW * 8 * NT) * (D + 4) * 4;
 }
 
-// NT: 8-row groups of query rows per warp; R: warps that share a tile stream,
-// each with its own rows (8·NT·R ≥ G·T).
+// R: warps that share a tile stream, each with its own rows (8·NT·R ≥ G·T).
 template <int D, int NT, int R, bool Q4>
-__global__ void __launch_bounds__(Shape<D, Q4>::threads, 2)
+__global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
     mod_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, ModArgs a) {
-  using Sh = Shape<D, Q4>;
-  constexpr int NW = Sh::NW, NS = NW / R, ST = mod_stages<D, NT, R, Q4>(), KS = D / 16, MT = D / 16, PITCH = D + 4;
+  using Sh = Shape<D, NT, Q4>;
+  constexpr int NW = Sh::NW, U = Sh::U, NS = NW / R, ST = mod_stages<D, NT, R, Q4>();
+  constexpr int KS = D / 16, MT = D / 16, PITCH = D + 4;
   static_assert(ST >= 2 && NW % R == 0, "ring too small");
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t bars[NS * ST];
@@ -298,43 +308,55 @@ __global__ void __launch_bounds__(Shape<D, Q4>::threads, 2)
 
   unsigned char* my_ring = ring + stream * ST * Sh::slot_bytes;
   uint64_t* my_bar = bars + stream * ST;
-  int it = 0;  // tiles this stream has consumed: ring position and parity
+  int it = 0;  // steps this stream has consumed: ring position and parity
   Tile cur, nxt;
-  auto issue = [&](Tile src, int n) {  // lane 0 of the stream's first warp: tile src into ring position n
+  auto issue = [&](const Tile (&src)[U], int n) {  // lane 0 of the stream's first warp: a step into ring position n
     const int sl = n % ST;
     unsigned char* dst = my_ring + sl * Sh::slot_bytes;
-    if (src.at < 0) {
-      mbar_arrive(&my_bar[sl]);
-      return;
-    }
-    mbar_arrive_expect_tx(&my_bar[sl], Sh::tile_bytes);
-    if constexpr (Q4) {
-      bulk_g2s(dst, a.pool + static_cast<size_t>(src.at) * Sh::tile_bytes, Sh::tile_bytes, &my_bar[sl]);
-    } else {
+    int tiles = 0;
 #pragma unroll
-      for (int half = 0; half < D / 64; ++half) {
-        tma_2d(dst + half * kTile * 128, &kmap, half * 64, src.at * kTile, &my_bar[sl]);
-        tma_2d(dst + (D / 64 + half) * kTile * 128, &vmap, half * 64, src.at * kTile, &my_bar[sl]);
+    for (int u = 0; u < U; ++u) tiles += src[u].at >= 0 ? 1 : 0;
+    mbar_arrive_expect_tx(&my_bar[sl], static_cast<unsigned int>(tiles * Sh::tile_bytes));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (src[u].at < 0) continue;
+      if constexpr (Q4) {
+        bulk_g2s(dst + u * (Sh::slot_bytes / U), a.pool + static_cast<size_t>(src[u].at) * Sh::tile_bytes,
+                 Sh::tile_bytes, &my_bar[sl]);
+      } else {
+#pragma unroll
+        for (int half = 0; half < D / 64; ++half) {
+          tma_2d(dst + half * kTile * 128, &kmap, half * 64, src[u].at * kTile, &my_bar[sl]);
+          tma_2d(dst + (D / 64 + half) * kTile * 128, &vmap, half * 64, src[u].at * kTile, &my_bar[sl]);
+        }
       }
     }
   };
-  auto stream_tiles = [&](const Segment& s) {
-    const int n = s.t1 - s.t0 - stream;
-    return n > 0 ? (n + NS - 1) / NS : 0;
+  // A stream's step k is tiles t0 + U·(stream + NS·k) .. + U − 1; a lookup
+  // resolves the 32 tiles of 32/U steps, one per lane.
+  constexpr int kSteps = 32 / U;
+  auto stream_steps = [&](const Segment& s) {
+    const int n = s.t1 - s.t0 - U * stream;
+    return n > 0 ? (n + U * NS - 1) / (U * NS) : 0;
   };
-  auto lookup = [&](const Segment& s, int batch32) {
-    return resolve_tile(a, s, s.t0 + stream + NS * (32 * batch32 + lane));
+  auto lookup = [&](const Segment& s, int batch) {
+    return resolve_tile(a, s, s.t0 + U * (stream + NS * (kSteps * batch + lane / U)) + lane % U);
   };
-  auto pick = [&](const Tile& x, int k) {
-    return Tile{__shfl_sync(0xffffffffu, x.at, k & 31), __shfl_sync(0xffffffffu, x.j0, k & 31)};
+  auto pick = [&](const Tile& x, int k, Tile (&to)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int from = (k % kSteps) * U + u;
+      to[u] = Tile{__shfl_sync(0xffffffffu, x.at, from), __shfl_sync(0xffffffffu, x.j0, from)};
+    }
   };
   auto prologue = [&](const Segment& s) {
-    const int nk = stream_tiles(s);
+    const int nk = stream_steps(s);
     cur = lookup(s, 0);
     nxt = lookup(s, 1);
 #pragma unroll
     for (int k = 0; k < ST; ++k) {
-      const Tile x = pick(cur, k);
+      Tile x[U];
+      pick(cur, k, x);
       if (lane == 0 && rg == 0 && k < nk) issue(x, it + k);
     }
   };
@@ -359,7 +381,7 @@ __global__ void __launch_bounds__(Shape<D, Q4>::threads, 2)
     if (a.slopes) ref = make_int2(tile_position(a, seg, seg.t0), tile_position(a, seg, seg.t1 - 1) + kTile - 1);
     int dist0[NT][2];
     uint32_t qf[KS][NT][2];
-    float qsum[NT][2];
+    float qsum[NT][2], qdown[NT][2];  // 4 bits: (Σ q)·factor, factor/2^k of the lane's columns
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -376,7 +398,6 @@ __global__ void __launch_bounds__(Shape<D, Q4>::threads, 2)
       }
       const int row = (rg * NT + nt) * 8 + g, rr = row < rows ? row : 0, t = rr / a.G;
       const bf16* qp = a.q + ((static_cast<size_t>(seg.b) * a.T + t) * a.Hq + seg.h * a.G + rr - t * a.G) * D;
-      float sum = 0.f;
       if constexpr (!Q4) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -384,24 +405,39 @@ __global__ void __launch_bounds__(Shape<D, Q4>::threads, 2)
           qf[ks][nt][1] = *reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8 + 2 * t4);
         }
       } else {
-        // the k order of the codes: word w of lane t4's share (D/4 numbers from
-        // D/4·t4) gives the pairs (8w + i, 8w + i + 4)
+        // fp16, scaled by a power of two to a largest number in [2^14, 2^15): bf16's
+        // 8 bits fit, and what falls below fp16's range is under 2^-38 of the
+        // largest.  The k order is that of the codes: word w of lane t4's share
+        // (D/4 numbers from D/4·t4) gives the pairs (8w + i, 8w + i + 4); codes at
+        // odd i come 16 times too large, so their numbers are divided by 16.
+        float x[D / 4], sum = 0.f, top = 0.f;
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) {
-          const uint4 x = *reinterpret_cast<const uint4*>(qp + D / 4 * t4 + 8 * w);
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+        for (int w = 0; w < D / 32; ++w) load8(qp + D / 4 * t4 + 8 * w, x + 8 * w);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t lo = xs[i >> 1], hi = xs[2 + (i >> 1)];
-            qf[2 * w + (i >> 1)][nt][i & 1] = __byte_perm(lo, hi, (i & 1) ? 0x7632 : 0x5410);
-            sum += bf16_lo(xs[i]) + bf16_hi(xs[i]);
-          }
+        for (int i = 0; i < D / 4; ++i) {
+          sum += x[i];
+          top = fmaxf(top, fabsf(x[i]));
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int k = min(126, 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23));
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + max(k, -126)) << 23);
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float by = (i & 1) ? up * 0.0625f : up;
+            const __half2 h = __floats2half2_rn(x[8 * w + i] * by, x[8 * w + i + 4] * by);
+            qf[2 * w + (i >> 1)][nt][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        const float zf = a.cap2 != 0.f ? a.capx : a.scale2, down = zf / up;
+        qsum[nt][0] = __shfl_sync(0xffffffffu, sum * zf, 8 * t4);
+        qsum[nt][1] = __shfl_sync(0xffffffffu, sum * zf, 8 * t4 + 4);
+        qdown[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t4);
+        qdown[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t4 + 4);
       }
-      qsum[nt][0] = __shfl_sync(0xffffffffu, sum, 8 * t4);
-      qsum[nt][1] = __shfl_sync(0xffffffffu, sum, 8 * t4 + 4);
     }
 
     float o[MT][NT][4], m_sub[NT][2], m_lim[NT][2], l[NT][2], corr[NT][2];
@@ -418,50 +454,57 @@ __global__ void __launch_bounds__(Shape<D, Q4>::threads, 2)
     }
 
     // ---- the tiles
-    const int nk = stream_tiles(seg);
-    const int i_first = seg.vis.L - a.T, i_last = seg.vis.L - 1;
+    const int nk = stream_steps(seg);
+    const int i_first = seg.vis.L - a.T;
     for (int k = 0; k < nk; ++k, ++it) {
-      if (k > 0 && (k & 31) == 0) {
+      if (k > 0 && k % kSteps == 0) {
         cur = nxt;
-        nxt = lookup(seg, (k >> 5) + 1);
+        nxt = lookup(seg, k / kSteps + 1);
       }
-      const Tile tl = pick(cur, k);
+      Tile tl[U];
+      pick(cur, k, tl);
       const int sl = it % ST;
       const unsigned int parity = static_cast<unsigned int>(it / ST) & 1u;
       if (!mbar_wait(&my_bar[sl], parity)) mbar_wait(&my_bar[sl], parity);
-      if (tl.at >= 0) {
-        unsigned char* buf = my_ring + sl * Sh::slot_bytes;
-        // scores
-        float z[NT][4];
-        float vs[2], vmid[2];  // 4 bits: V's step and the value of code 8, of tokens g and g + 8
-        if constexpr (!Q4) {
+      unsigned char* const buf = my_ring + sl * Sh::slot_bytes;
+      bool whole = true;
+#pragma unroll
+      for (int u = 0; u < U; ++u) whole = whole && (tl[u].j0 & 1) != 0;
+
+      // scores: Sᵀ of the step's tiles, in base 2 when there is no cap, else over the cap
+      float z[U][NT][4];
+      if constexpr (!Q4) {
+        float z2[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[0][nt][e] = z2[nt][e] = 0.f;
+        const uint32_t kbase = smem_addr(buf);
+        const int tok = lane & 15, ch = lane >> 4;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const int c = 2 * ks + ch;
+          uint32_t af[4];
+          ldsm_x4(kbase + (c >> 3) * (kTile * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4), af);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_bf16(ks & 1 ? z2[nt] : z[0][nt], af, qf[ks][nt][0], qf[ks][nt][1]);
+        }
+        const float zf = a.cap2 != 0.f ? a.capx : a.scale2;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[0][nt][e] = (z[0][nt][e] + z2[nt][e]) * zf;
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const unsigned char* rec = buf + u * (Sh::slot_bytes / U);
           float z2[NT][4];
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[nt][e] = z2[nt][e] = 0.f;
-          const uint32_t kbase = smem_addr(buf);
-          const int tok = lane & 15, ch = lane >> 4;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            const int c = 2 * ks + ch;
-            uint32_t af[4];
-            ldsm_x4(kbase + (c >> 3) * (kTile * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4), af);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_bf16(ks & 1 ? z2[nt] : z[nt], af, qf[ks][nt][0], qf[ks][nt][1]);
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[nt][e] += z2[nt][e];
-        } else {
-          float z2[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[nt][e] = z2[nt][e] = 0.f;
+            for (int e = 0; e < 4; ++e) z[u][nt][e] = z2[nt][e] = 0.f;
           uint32_t w0[D / 32], w1[D / 32];
-          const unsigned char* k0 = buf + g * (D / 2) + t4 * (D / 8);
+          const unsigned char* k0 = rec + g * (D / 2) + t4 * (D / 8);
           if constexpr (D == 128) {
             const uint4 x = *reinterpret_cast<const uint4*>(k0), y = *reinterpret_cast<const uint4*>(k0 + 8 * (D / 2));
             w0[0] = x.x; w0[1] = x.y; w0[2] = x.z; w0[3] = x.w;
@@ -471,133 +514,155 @@ __global__ void __launch_bounds__(Shape<D, Q4>::threads, 2)
             w0[0] = x.x; w0[1] = x.y;
             w1[0] = y.x; w1[1] = y.y;
           }
-          const uint32_t* pairs = reinterpret_cast<const uint32_t*>(buf + 16 * D);
-          const uint32_t ka = pairs[g], kb = pairs[g + 8], va = pairs[16 + g], vb = pairs[24 + g];
+          const uint32_t* pairs = reinterpret_cast<const uint32_t*>(rec + 16 * D);
+          const uint32_t ka = pairs[g], kb = pairs[g + 8];
 #pragma unroll
           for (int w = 0; w < D / 32; ++w)
 #pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              const uint32_t af[4] = {q4_pair(w0[w], i), q4_pair(w1[w], i), q4_pair(w0[w], i + 1), q4_pair(w1[w], i + 1)};
-              const int ks = 2 * w + (i >> 1);
+            for (int b = 0; b < 2; ++b) {  // codes 0, 1, 4, 5 of a word, then 2, 3, 6, 7
+              const uint32_t x = w0[w] >> (8 * b), y = w1[w] >> (8 * b);
+              const uint32_t af[4] = {q4_half_low(x), q4_half_low(y), q4_half_high(x), q4_half_high(y)};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_bf16(ks & 1 ? z2[nt] : z[nt], af, qf[ks][nt][0], qf[ks][nt][1]);
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(b ? z2[nt] : z[u][nt], af, qf[2 * w + b][nt][0], qf[2 * w + b][nt][1]);
             }
           const float ks0 = bf16_lo(ka), ks1 = bf16_lo(kb);
           const float km0 = fmaf(8.f, ks0, bf16_hi(ka)), km1 = fmaf(8.f, ks1, bf16_hi(kb));
-          vs[0] = bf16_lo(va);
-          vs[1] = bf16_lo(vb);
-          vmid[0] = fmaf(8.f, vs[0], bf16_hi(va));
-          vmid[1] = fmaf(8.f, vs[1], bf16_hi(vb));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              z[nt][e] = fmaf(ks0, z[nt][e] + z2[nt][e], km0 * qsum[nt][e]);
-              z[nt][2 + e] = fmaf(ks1, z[nt][2 + e] + z2[nt][2 + e], km1 * qsum[nt][e]);
+              z[u][nt][e] = fmaf(ks0, (z[u][nt][e] + z2[nt][e]) * qdown[nt][e], km0 * qsum[nt][e]);
+              z[u][nt][2 + e] = fmaf(ks1, (z[u][nt][2 + e] + z2[nt][2 + e]) * qdown[nt][e], km1 * qsum[nt][e]);
             }
         }
-        // cap, bias
+      }
+      if (a.cap2 != 0.f) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            z[nt][e] = a.cap2 != 0.f ? a.cap2 * tanh_f32(z[nt][e] * a.capx) : z[nt][e] * a.scale2;
-        if (a.slopes) {
+        for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = tl.j0 + g + (e >> 1) * 8;
-              z[nt][e] = fmaf(-slope2[nt][e & 1], static_cast<float>(abs(qi[nt][e & 1] - j) - dist0[nt][e & 1]), z[nt][e]);
+            for (int e = 0; e < 4; ++e) z[u][nt][e] = a.cap2 * tanh_f32(z[u][nt][e]);
+      }
+      if (a.slopes) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int far = qi[nt][e] - (tl[u].j0 & -kTile), near = far - 15;
+              if (near >= 0) {  // the whole tile lies behind the query: the bias is linear
+                const float at = static_cast<float>(far - dist0[nt][e]) - static_cast<float>(g);
+                z[u][nt][e] = fmaf(-slope2[nt][e], at, z[u][nt][e]);
+                z[u][nt][2 + e] = fmaf(-slope2[nt][e], at - 8.f, z[u][nt][2 + e]);
+              } else {
+                z[u][nt][e] = fmaf(-slope2[nt][e], static_cast<float>(abs(far - g) - dist0[nt][e]), z[u][nt][e]);
+                z[u][nt][2 + e] = fmaf(-slope2[nt][e], static_cast<float>(abs(far - g - 8) - dist0[nt][e]), z[u][nt][2 + e]);
+              }
             }
-        }
-        // masks: only tiles that not every row sees whole
-        const bool whole = tl.j0 >= seg.vis.start &&
-                           (tl.j0 + kTile <= seg.vis.prefix ||
-                            (tl.j0 + kTile - 1 <= i_first && (a.window <= 0 || i_last - tl.j0 < a.window)));
-        uint32_t apart = 0;  // bf16: tokens that some rows see and others do not, with a V that is not finite
-        if (!whole) {
-          auto sees = [&](int i, int j) {
-            return j >= seg.vis.start && i >= 0 && j < seg.vis.L &&
-                   (j < seg.vis.prefix || (j <= i && (a.window <= 0 || i - j < a.window)));
-          };
+      }
+      // masks: only steps that not every row sees whole
+      uint32_t apart = 0;  // bf16: tokens that some rows see and others do not, with a V that is not finite
+      if (!whole) {
+        auto sees = [&](int i, int j) {
+          return j >= seg.vis.start && i >= 0 && j < seg.vis.L &&
+                 (j < seg.vis.prefix || (j <= i && (a.window <= 0 || i - j < a.window)));
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (!sees(qi[nt][e & 1], tl.j0 + g + (e >> 1) * 8)) z[nt][e] = -INFINITY;
-          if constexpr (!Q4) {
-            // 0·V must not turn a masked NaN into the sum: rows of V that nobody
-            // sees are zeroed; a row only some see is set apart if it has one
-            bool any = false, all = true;
-            if (lane < kTile)
-              for (int t = 0; t < a.T; ++t) {
-                const bool v = sees(i_first + t, tl.j0 + lane);
-                any |= v;
-                all &= v;
-              }
-            const uint32_t seen = __ballot_sync(0xffffffffu, any && lane < kTile);
-            uint32_t some = seen & ~__ballot_sync(0xffffffffu, all && lane < kTile);
-            unsigned char* vt = buf + D / 64 * kTile * 128;
-            for (uint32_t rest = ~seen & 0xffffu; rest; rest &= rest - 1) {
-              const int tok = __ffs(rest) - 1;
-              if (lane < D / 8)
-                *reinterpret_cast<uint4*>(vt + (lane >> 3) * (kTile * 128) + tok * 128 + (lane & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
+              if (!sees(qi[nt][e & 1], (tl[u].j0 & -kTile) + g + (e >> 1) * 8)) z[u][nt][e] = -INFINITY;
+        if constexpr (!Q4) {
+          // 0·V must not turn a masked NaN into the sum: rows of V that nobody
+          // sees are zeroed; a row only some see is set apart if it has one
+          bool any = false, all = true;
+          if (lane < kTile)
+            for (int t = 0; t < a.T; ++t) {
+              const bool v = sees(i_first + t, (tl[0].j0 & -kTile) + lane);
+              any |= v;
+              all &= v;
             }
-            for (; some; some &= some - 1) {
-              const int tok = __ffs(some) - 1;
-              bool bad = false;
-              if (lane < D / 8) {
-                const uint4 x = *reinterpret_cast<const uint4*>(vt + (lane >> 3) * (kTile * 128) + tok * 128 + (lane & 7) * 16);
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  bad |= (xs[i] & 0x7f80u) == 0x7f80u || (xs[i] & 0x7f800000u) == 0x7f800000u;
-              }
-              if (__any_sync(0xffffffffu, bad)) apart |= 1u << tok;
-            }
-            __syncwarp();
+          const uint32_t seen = __ballot_sync(0xffffffffu, any && lane < kTile);
+          uint32_t some = seen & ~__ballot_sync(0xffffffffu, all && lane < kTile);
+          unsigned char* vt = buf + D / 64 * kTile * 128;
+          for (uint32_t rest = ~seen & 0xffffu; rest; rest &= rest - 1) {
+            const int tok = __ffs(rest) - 1;
+            if (lane < D / 8)
+              *reinterpret_cast<uint4*>(vt + (lane >> 3) * (kTile * 128) + tok * 128 + (lane & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
           }
+          for (; some; some &= some - 1) {
+            const int tok = __ffs(some) - 1;
+            bool bad = false;
+            if (lane < D / 8) {
+              const uint4 x = *reinterpret_cast<const uint4*>(vt + (lane >> 3) * (kTile * 128) + tok * 128 + (lane & 7) * 16);
+              const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                bad |= (xs[i] & 0x7f80u) == 0x7f80u || (xs[i] & 0x7f800000u) == 0x7f800000u;
+            }
+            if (__any_sync(0xffffffffu, bad)) apart |= 1u << tok;
+          }
+          __syncwarp();
         }
-        // a score far above the reference: new maxima, and the state follows
-        bool grow = false;
+      }
+      // a score far above the reference: new maxima, and the state follows
+      bool grow = false;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) grow |= z[nt][e] > m_lim[nt][e & 1];
-        if (__any_sync(0xffffffffu, grow)) {
+          for (int e = 0; e < 4; ++e) grow |= z[u][nt][e] > m_lim[nt][e & 1];
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float top = fmaxf(z[nt][e], z[nt][2 + e]);
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-              const float old = m_lim[nt][e] - kGrow;  // −inf at first
-              if (top > old) {
-                const float f = ex2(old - top);
-                m_sub[nt][e] = top;
-                m_lim[nt][e] = top + kGrow;
-                l[nt][e] *= f;
-                corr[nt][e] *= f;
+          for (int e = 0; e < 2; ++e) {
+            float top = fmaxf(z[0][nt][e], z[0][nt][2 + e]);
+            if constexpr (U == 2) top = fmaxf(top, fmaxf(z[U - 1][nt][e], z[U - 1][nt][2 + e]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float old = m_lim[nt][e] - kGrow;  // −inf at first
+            if (top > old) {
+              const float f = ex2(old - top);
+              m_sub[nt][e] = top;
+              m_lim[nt][e] = top + kGrow;
+              l[nt][e] *= f;
+              corr[nt][e] *= f;
 #pragma unroll
-                for (int j = 0; j < MT; ++j) {
-                  o[j][nt][e] *= f;
-                  o[j][nt][2 + e] *= f;
-                }
+              for (int j = 0; j < MT; ++j) {
+                o[j][nt][e] *= f;
+                o[j][nt][2 + e] *= f;
               }
             }
+          }
+      }
+      // weights, and their three bf16 parts as B fragments
+      uint32_t pf[U][NT][3][2];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float vs[2], vmid[2];  // 4 bits: V's step and the value of code 8, of tokens g and g + 8
+        if constexpr (Q4) {
+          const uint32_t* pairs = reinterpret_cast<const uint32_t*>(buf + u * (Sh::slot_bytes / U) + 16 * D);
+          const uint32_t va = pairs[16 + g], vb = pairs[24 + g];
+          vs[0] = bf16_lo(va);
+          vs[1] = bf16_lo(vb);
+          vmid[0] = fmaf(8.f, vs[0], bf16_hi(va));
+          vmid[1] = fmaf(8.f, vs[1], bf16_hi(vb));
         }
-        // weights, and their three bf16 parts as B fragments
-        uint32_t pf[NT][3][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            p[e] = ex2(z[nt][e] - m_sub[nt][e & 1]);
+            p[e] = ex2(z[u][nt][e] - m_sub[nt][e & 1]);
             l[nt][e & 1] += p[e];
           }
           if constexpr (!Q4) {
@@ -620,58 +685,90 @@ __global__ void __launch_bounds__(Shape<D, Q4>::threads, 2)
                   }
               }
             }
-          } else {
+          } else if (whole) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              // a masked token's pair may hold anything
-              const bool on = whole || p[e] > 0.f;
-              if (on) corr[nt][e & 1] = fmaf(p[e], vmid[e >> 1], corr[nt][e & 1]);
-              p[e] = on ? p[e] * vs[e >> 1] : 0.f;
+              corr[nt][e & 1] = fmaf(p[e], vmid[e >> 1], corr[nt][e & 1]);
+              p[e] *= vs[e >> 1];
+            }
+          } else {  // a masked token's pair may hold anything
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (p[e] > 0.f) corr[nt][e & 1] = fmaf(p[e], vmid[e >> 1], corr[nt][e & 1]);
+              p[e] = p[e] > 0.f ? p[e] * vs[e >> 1] : 0.f;
             }
           }
 #pragma unroll
           for (int part = 0; part < 3; ++part) {
-            pf[nt][part][0] = transpose8x8(__byte_perm(__float_as_uint(p[0]), __float_as_uint(p[1]), 0x7632));
-            pf[nt][part][1] = transpose8x8(__byte_perm(__float_as_uint(p[2]), __float_as_uint(p[3]), 0x7632));
+            pf[u][nt][part][0] = transpose8x8(__byte_perm(__float_as_uint(p[0]), __float_as_uint(p[1]), 0x7632));
+            pf[u][nt][part][1] = transpose8x8(__byte_perm(__float_as_uint(p[2]), __float_as_uint(p[3]), 0x7632));
             if (part < 2) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) p[e] -= __uint_as_float(__float_as_uint(p[e]) & 0xffff0000u);
+              for (int e = 0; e < 4; ++e) {
+                p[e] -= __uint_as_float(__float_as_uint(p[e]) & 0xffff0000u);
+                if (Q4 && part == 0) corr[nt][e & 1] = fmaf(-24.f, p[e], corr[nt][e & 1]);
+              }
             }
           }
         }
-        if constexpr (!Q4) {
-          if (apart) {
-            stream_sync();  // the warps that share the tile have all read the rows
-            unsigned char* vt = buf + D / 64 * kTile * 128;
-            for (uint32_t rest = apart; rest; rest &= rest - 1) {
-              const int tok = __ffs(rest) - 1;
-              if (lane < D / 8)
-                *reinterpret_cast<uint4*>(vt + (lane >> 3) * (kTile * 128) + tok * 128 + (lane & 7) * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            }
-            __syncwarp();
+      }
+      if constexpr (!Q4) {
+        if (apart) {
+          stream_sync();  // the warps that share the tile have all read the rows
+          unsigned char* vt = buf + D / 64 * kTile * 128;
+          for (uint32_t rest = apart; rest; rest &= rest - 1) {
+            const int tok = __ffs(rest) - 1;
+            if (lane < D / 8)
+              *reinterpret_cast<uint4*>(vt + (lane >> 3) * (kTile * 128) + tok * 128 + (lane & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
+          __syncwarp();
+        }
+      }
+      // p·v.  The tensor cores drop bits when they add to an accumulator; over
+      // thousands of tokens that shrinks it by 1e-5 and more.  So each step's
+      // product starts afresh and is added with rounding.
+      if constexpr (!Q4) {
+        const uint32_t vbase = smem_addr(buf) + D / 64 * kTile * 128;
+        const int tok = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          const int c = 2 * j + ch;
+          uint32_t af[4];
+          ldsm_x4_trans(vbase + (c >> 3) * (kTile * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4), af);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int part = 2; part >= 0; --part) mma_bf16(t, af, pf[0][nt][part][0], pf[0][nt][part][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][nt][e] += t[e];
           }
         }
-        // p·v
-        if constexpr (!Q4) {
-          const uint32_t vbase = smem_addr(buf) + D / 64 * kTile * 128;
-          const int tok = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
+      } else {
+        // The codes enter as 16 + n (no subtraction): products with the first
+        // part of p start from −24·Σ hi, computed by the same tensor cores from a
+        // tile of −24, and give Σ hi·(n − 8) without loss, since hi has 8 bits;
+        // the other parts leave 24·Σ (mid + lo), small, which corr takes back.
+        float c24[NT][4];
+        const uint32_t m24[4] = {0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u};
 #pragma unroll
-          for (int j = 0; j < MT; ++j) {
-            const int c = 2 * j + ch;
-            uint32_t af[4];
-            ldsm_x4_trans(vbase + (c >> 3) * (kTile * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4), af);
+        for (int nt = 0; nt < NT; ++nt) {
+          c24[nt][0] = c24[nt][1] = c24[nt][2] = c24[nt][3] = 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) add_product(o[j][nt], af, pf[nt]);
-          }
-        } else {
-          // lane (g, t4): tokens 2·t4, 2·t4 + 1 (+ 8), numbers D/8·g … of each;
-          // the byte interleave pairs the two tokens' codes of one number
-          constexpr int VW = D / 64;  // words per lane and token
+          for (int u = 0; u < U; ++u) mma_bf16(c24[nt], m24, pf[u][nt][0][0], pf[u][nt][0][1]);
+        }
+        // lane (g, t4): tokens 2·t4, 2·t4 + 1 (+ 8), numbers D/8·g … of each;
+        // the byte interleave pairs the two tokens' codes of one number
+        constexpr int VW = D / 64;  // words per lane and token
+        uint32_t un[U][2][2 * VW];  // [tokens, tokens + 8][four numbers each]
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
           uint32_t wv[4][VW];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const unsigned char* src = buf + 8 * D + (2 * t4 + (x & 1) + (x >> 1) * 8) * (D / 2) + g * (D / 16);
+            const unsigned char* src = buf + u * (Sh::slot_bytes / U) + 8 * D +
+                                       (2 * t4 + (x & 1) + (x >> 1) * 8) * (D / 2) + g * (D / 16);
             if constexpr (VW == 2) {
               const uint2 y = *reinterpret_cast<const uint2*>(src);
               wv[x][0] = y.x;
@@ -680,28 +777,42 @@ __global__ void __launch_bounds__(Shape<D, Q4>::threads, 2)
               wv[x][0] = *reinterpret_cast<const uint32_t*>(src);
             }
           }
-          uint32_t un[2][2 * VW];  // [tokens, tokens + 8][four numbers each]
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
-              un[hf][2 * w] = __byte_perm(wv[2 * hf][w], wv[2 * hf + 1][w], 0x5410);
-              un[hf][2 * w + 1] = __byte_perm(wv[2 * hf][w], wv[2 * hf + 1][w], 0x7632);
+              un[u][hf][2 * w] = __byte_perm(wv[2 * hf][w], wv[2 * hf + 1][w], 0x5410);
+              un[u][hf][2 * w + 1] = __byte_perm(wv[2 * hf][w], wv[2 * hf + 1][w], 0x7632);
             }
+        }
 #pragma unroll
-          for (int j = 0; j < MT; ++j) {
-            // m rows g: number j of the lane's share; rows g + 8: number MT + j
-            const uint32_t af[4] = {q4_pair(un[0][j / 4], j & 3), q4_pair(un[0][MT / 4 + j / 4], j & 3),
-                                    q4_pair(un[1][j / 4], j & 3), q4_pair(un[1][MT / 4 + j / 4], j & 3)};
+        for (int j = 0; j < MT; ++j) {
+          // m rows g: number j of the lane's share; rows g + 8: number MT + j
+          uint32_t af[U][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) add_product(o[j][nt], af, pf[nt]);
+          for (int u = 0; u < U; ++u) {
+            af[u][0] = q4_pair16(un[u][0][j / 4], j & 3);
+            af[u][1] = q4_pair16(un[u][0][MT / 4 + j / 4], j & 3);
+            af[u][2] = q4_pair16(un[u][1][j / 4], j & 3);
+            af[u][3] = q4_pair16(un[u][1][MT / 4 + j / 4], j & 3);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float t[4] = {c24[nt][0], c24[nt][1], c24[nt][2], c24[nt][3]};
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+              for (int u = 0; u < U; ++u) mma_bf16(t, af[u], pf[u][nt][part][0], pf[u][nt][part][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][nt][e] += t[e];
           }
         }
       }
-      // the slot is free: the next copy into it
+      // the slot is free: the next copies into it
       stream_sync();
       const int ahead = k + ST;
-      const Tile x = pick((ahead >> 5) == (k >> 5) ? cur : nxt, ahead);
+      Tile x[U];
+      pick(ahead / kSteps == k / kSteps ? cur : nxt, ahead, x);
       if (lane == 0 && rg == 0 && ahead < nk) {
         fence_proxy_async_shared();  // the slot's reads come before the copies that refill it
         issue(x, it + ST);
@@ -897,7 +1008,7 @@ cudaError_t run_mod(const ModArgs& a, const CUtensorMap& km, const CUtensorMap& 
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int ctas = min(kModCtas, 2 * sm_count());
-  e = launch_k(mod_kernel<D, NT, R, Q4>, dim3(static_cast<unsigned>(ctas)), Shape<D, Q4>::threads, smem, st, km, vm, a);
+  e = launch_k(mod_kernel<D, NT, R, Q4>, dim3(static_cast<unsigned>(ctas)), Shape<D, NT, Q4>::threads, smem, st, km, vm, a);
   if (e != cudaSuccess) return e;
   return launch_k(mod_combine_kernel<D>, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(a.G * a.T)), 4 * D, 0,
                   st, a);
