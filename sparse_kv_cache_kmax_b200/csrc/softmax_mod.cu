@@ -34,6 +34,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr int kModCtas = 296;     // two resident CTAs on each of 148 SMs: one wave
 constexpr float kGrow = 8.0f;     // a score may pass the reference maximum by 2^8 before the state is rescaled
+constexpr float kNoMax = -3e38f;  // before the first score
 
 struct ModArgs {
   const int32_t* page_table;
@@ -54,7 +55,9 @@ struct ModArgs {
   float scale2;  // scale·log2(e), the factor of q·k without a cap
   float capx;    // scale/softcap
   float cap2;    // softcap·log2(e); 0: no cap
-  int window, batch, Hkv, Hq, G, T, S, num_phys, max_pages, cap, min_tiles;
+  int window, batch, Hkv, Hq, G, T, S, num_phys, max_pages, cap;
+  int min_tiles;    // the smallest run of a CTA
+  int slack_tiles;  // how much longer a run may get where no CTA then crosses units
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -75,13 +78,31 @@ __device__ __forceinline__ float tanh_f32(float x) {
   return x != x ? x : copysignf(t, x);
 }
 
-// As mma_bf16, with fp16 operands.
-__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// d = A·B + c on m16n8k16 (fragments as mma_bf16 in common.cuh), bf16 or fp16
+// operands.  d and c apart, and no volatile: the compiler is free to interleave
+// the products of several rows.
+template <bool Half>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2], float c0, float c1,
+                                    float c2, float c3) {
+  if constexpr (Half)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+template <bool Half>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2],
+                                    const float (&c)[4]) {
+  mma<Half>(d, a, b, c[0], c[1], c[2], c[3]);
+}
+template <bool Half>
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  mma<Half>(d, a, b, 0.f, 0.f, 0.f, 0.f);
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -138,16 +159,18 @@ __device__ __forceinline__ int group_tiles(const ModArgs& a, int grp) {
   return max(1, max(0, min(a.n_sel[grp], a.cap)) * (a.S / kTile));
 }
 
-// The part of a unit that this CTA works on: tiles t0 .. t1−1 of n.
+// The part of a unit that a CTA works on: tiles t0 .. t1−1 of n, one of
+// `pieces` parts (the first one of them knows how many).
 struct Segment {
   Visible vis;
-  int unit, b, h, t0, t1, n;
+  int unit, b, h, t0, t1, n, pieces;
 };
 
 // The physical place of a tile (row of the pools, or record of the 4-bit pool)
 // and the position of its first token, a multiple of 16; bit 0 of j0 says that
-// every row sees all of it, so that most tiles need no masks.  at = −1: nothing
-// there to see, and a position that no mask lets through.
+// every row sees all of it, so that most tiles need no masks, bit 1 that it lies
+// behind every row.  at = −1: nothing there to see, and a position that no mask
+// lets through.
 struct Tile {
   int at, j0;
 };
@@ -184,7 +207,7 @@ __device__ __forceinline__ Tile resolve_tile(const ModArgs& a, const Segment& s,
   const bool whole = j0 >= s.vis.start &&
                      (j0 + kTile <= s.vis.prefix ||
                       (j0 + kTile <= s.vis.L - a.T + 1 && (a.window <= 0 || s.vis.L - 1 - j0 < a.window)));
-  r.j0 = j0 | (whole ? 1 : 0);
+  r.j0 = j0 | (whole ? 1 : 0) | (j0 + kTile <= s.vis.L - a.T + 1 ? 2 : 0);
   return r;
 }
 
@@ -248,7 +271,11 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   __shared__ uint64_t bars[NS * ST];
   __shared__ float s_m[NW][8 * NT], s_l[NW][8 * NT], s_c[NW][8 * NT];
   __shared__ int scan_s[33];
-  __shared__ long long s_at[3];  // group, its first tile, total
+  __shared__ Segment s_seg[2];  // the unit in work, and the next
+  __shared__ struct {
+    long long at;  // start of the group in the list
+    int grp, tiles;
+  } s_found;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int stream = warp / R, rg = warp - stream * R;
@@ -261,73 +288,110 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   }
   grid_dep_enter();
 
-  // this CTA's run of the work list
+  // This CTA's run of the work list.  Cutting the list into equal runs keeps
+  // every CTA equally busy but lets one cross units, which costs it a second
+  // set of queries and a second merge; cutting every unit into equal pieces
+  // costs nothing while there are CTAs enough, so that comes first.
   const int mult = a.sel ? 1 : a.Hkv, groups = a.sel ? a.batch * a.Hkv : a.batch;
-  long long total = 0;
-  for (int c0 = 0; c0 < groups; c0 += Sh::threads) {
-    int sum;
-    block_exclusive_scan(c0 + tid < groups ? group_tiles(a, c0 + tid) * mult : 0, scan_s, &sum);
-    total += sum;
-    __syncthreads();
+  const int mine0 = tid < groups ? group_tiles(a, tid) : 0;  // most batches: one group per thread
+  auto tiles_of = [&](int c0) { return c0 == 0 ? mine0 : (c0 + tid < groups ? group_tiles(a, c0 + tid) : 0); };
+  auto sum_over_groups = [&](auto value) {  // value(tiles), times the units of a group
+    long long total = 0;
+    for (int c0 = 0; c0 < groups; c0 += Sh::threads) {
+      int sum;
+      block_exclusive_scan(value(tiles_of(c0)) * mult, scan_s, &sum);
+      total += sum;
+      __syncthreads();
+    }
+    return total;
+  };
+  const long long total = sum_over_groups([](int n) { return n; });
+  const int ctas = static_cast<int>(gridDim.x);
+  int per = max(static_cast<int>((total + ctas - 1) / ctas), a.min_tiles);
+  bool aligned = false;
+  if (static_cast<long long>(groups) * mult <= ctas) {
+    auto pieces = [&](int by) { return sum_over_groups([by](int n) { return (n + by - 1) / by; }); };
+    aligned = pieces(per) <= ctas;
+    if (!aligned) {
+      // equal units: what the CTAs of one would take
+      const int units = groups * mult, each = ctas / units, by = (static_cast<int>(total / units) + each - 1) / each;
+      if (by >= per && by - per <= a.slack_tiles && pieces(by) <= ctas) {
+        aligned = true;
+        per = by;
+      }
+    }
   }
-  long long per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < a.min_tiles) per = a.min_tiles;
-  long long pos = per * blockIdx.x;
-  const long long end = pos + per < total ? pos + per : total;
-  if (tid == 0) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
-  if (pos >= total) return;
-  long long before = 0;
-  for (int c0 = 0; c0 < groups; c0 += Sh::threads) {
+  // the group that holds this CTA's start: counted in pieces, or in tiles
+  const long long start = aligned ? blockIdx.x : static_cast<long long>(per) * blockIdx.x;
+  long long pos = start, before = 0;
+  if (tid == 0) {
+    a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+    s_found.grp = -1;
+  }
+  __syncthreads();
+  for (int c0 = 0; c0 < groups && before <= start; c0 += Sh::threads) {
     int sum;
-    const int mine = c0 + tid < groups ? group_tiles(a, c0 + tid) * mult : 0;
+    const int n = tiles_of(c0), mine = (aligned ? (n + per - 1) / per : n) * mult;
     const int ex = block_exclusive_scan(mine, scan_s, &sum);
-    if (before + ex <= pos && pos < before + ex + mine) {
-      s_at[0] = c0 + tid;
-      s_at[1] = before + ex;
+    if (before + ex <= start && start < before + ex + mine) {
+      s_found.at = before + ex;
+      s_found.grp = c0 + tid;
+      s_found.tiles = n;
     }
     before += sum;
     __syncthreads();
-    if (before > pos) break;
   }
-  int grp = static_cast<int>(s_at[0]);
-  long long grp_at = s_at[1];
+  int grp = s_found.grp;
+  if (grp < 0) return;  // more CTAs than runs
+  long long grp_at = s_found.at;
+  const long long end = pos + per < total ? pos + per : total;  // of a run of tiles
 
-  auto load_group = [&](Segment& s) {  // the sequence (and unit) of grp
-    s.b = a.sel ? grp / a.Hkv : grp;
-    s.vis = visible_tiles(a, s.b);
-    s.n = a.sel ? max(1, max(0, min(a.n_sel[grp], a.cap)) * (a.S / kTile)) : max(1, s.vis.n);
-  };
-  auto place = [&](Segment& s) {  // the unit at pos
-    const int off = static_cast<int>(pos - grp_at), hh = off / s.n;
-    s.h = a.sel ? grp % a.Hkv : hh;
-    s.unit = s.b * a.Hkv + s.h;
-    s.t0 = off - hh * s.n;
-    const long long left = end - pos;
-    s.t1 = left < s.n - s.t0 ? s.t0 + static_cast<int>(left) : s.n;
+  Segment seg;  // the next one to work on; s_seg holds the one in work
+  seg.vis = visible_tiles(a, a.sel ? grp / a.Hkv : grp);
+  seg.n = s_found.tiles;
+  auto place = [&]() {  // the unit at pos of group grp
+    const int off = static_cast<int>(pos - grp_at);
+    seg.b = a.sel ? grp / a.Hkv : grp;
+    int hh;
+    if (aligned) {
+      const int np = (seg.n + per - 1) / per, piece = off % np;
+      hh = off / np;
+      seg.t0 = static_cast<int>(static_cast<long long>(seg.n) * piece / np);
+      seg.t1 = static_cast<int>(static_cast<long long>(seg.n) * (piece + 1) / np);
+      seg.pieces = np;
+    } else {
+      hh = off / seg.n;
+      seg.t0 = off - hh * seg.n;
+      const long long left = end - pos;
+      seg.t1 = left < seg.n - seg.t0 ? seg.t0 + static_cast<int>(left) : seg.n;
+      seg.pieces = static_cast<int>((pos - seg.t0 + seg.n - 1) / per) - static_cast<int>(blockIdx.x) + 1;
+    }
+    seg.h = a.sel ? grp % a.Hkv : hh;
+    seg.unit = seg.b * a.Hkv + seg.h;
   };
 
   unsigned char* my_ring = ring + stream * ST * Sh::slot_bytes;
   uint64_t* my_bar = bars + stream * ST;
   int it = 0;  // steps this stream has consumed: ring position and parity
   Tile cur, nxt;
-  auto issue = [&](const Tile (&src)[U], int n) {  // lane 0 of the stream's first warp: a step into ring position n
+  auto issue = [&](const int (&at)[U], int n) {  // lane 0 of the stream's first warp: a step into ring position n
     const int sl = n % ST;
     unsigned char* dst = my_ring + sl * Sh::slot_bytes;
     int tiles = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) tiles += src[u].at >= 0 ? 1 : 0;
+    for (int u = 0; u < U; ++u) tiles += at[u] >= 0 ? 1 : 0;
     mbar_arrive_expect_tx(&my_bar[sl], static_cast<unsigned int>(tiles * Sh::tile_bytes));
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (src[u].at < 0) continue;
+      if (at[u] < 0) continue;
       if constexpr (Q4) {
-        bulk_g2s(dst + u * (Sh::slot_bytes / U), a.pool + static_cast<size_t>(src[u].at) * Sh::tile_bytes,
-                 Sh::tile_bytes, &my_bar[sl]);
+        bulk_g2s(dst + u * (Sh::slot_bytes / U), a.pool + static_cast<size_t>(at[u]) * Sh::tile_bytes, Sh::tile_bytes,
+                 &my_bar[sl]);
       } else {
 #pragma unroll
         for (int half = 0; half < D / 64; ++half) {
-          tma_2d(dst + half * kTile * 128, &kmap, half * 64, src[u].at * kTile, &my_bar[sl]);
-          tma_2d(dst + (D / 64 + half) * kTile * 128, &vmap, half * 64, src[u].at * kTile, &my_bar[sl]);
+          tma_2d(dst + half * kTile * 128, &kmap, half * 64, at[u] * kTile, &my_bar[sl]);
+          tma_2d(dst + (D / 64 + half) * kTile * 128, &vmap, half * 64, at[u] * kTile, &my_bar[sl]);
         }
       }
     }
@@ -342,94 +406,116 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   auto lookup = [&](const Segment& s, int batch) {
     return resolve_tile(a, s, s.t0 + U * (stream + NS * (kSteps * batch + lane / U)) + lane % U);
   };
-  auto pick = [&](const Tile& x, int k, Tile (&to)[U]) {
+  auto pick = [&](int x, int k, int (&to)[U]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int from = (k % kSteps) * U + u;
-      to[u] = Tile{__shfl_sync(0xffffffffu, x.at, from), __shfl_sync(0xffffffffu, x.j0, from)};
-    }
+    for (int u = 0; u < U; ++u) to[u] = __shfl_sync(0xffffffffu, x, (k % kSteps) * U + u);
   };
-  auto prologue = [&](const Segment& s) {
+  const int rows = a.G * a.T;
+  // a lane's share of its query row (row g of each group of 8): bf16 caches, the
+  // B fragments; 4 bits, D/4 numbers from D/4·t4
+  uint32_t q_raw[NT][KS * 2];
+  auto prologue = [&](const Segment& s) {  // the unit's queries and first copies are on their way
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = (rg * NT + nt) * 8 + g, rr = row < rows ? row : 0, t = rr / a.G;
+      const bf16* qp = a.q + ((static_cast<size_t>(s.b) * a.T + t) * a.Hq + s.h * a.G + rr - t * a.G) * D;
+      if constexpr (Q4) {
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          const uint4 x = *reinterpret_cast<const uint4*>(qp + D / 4 * t4 + 8 * w);
+          q_raw[nt][4 * w] = x.x;
+          q_raw[nt][4 * w + 1] = x.y;
+          q_raw[nt][4 * w + 2] = x.z;
+          q_raw[nt][4 * w + 3] = x.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < KS * 2; ++i) q_raw[nt][i] = *reinterpret_cast<const uint32_t*>(qp + 8 * i + 2 * t4);
+      }
+    }
     const int nk = stream_steps(s);
     cur = lookup(s, 0);
-    nxt = lookup(s, 1);
 #pragma unroll
     for (int k = 0; k < ST; ++k) {
-      Tile x[U];
-      pick(cur, k, x);
-      if (lane == 0 && rg == 0 && k < nk) issue(x, it + k);
+      int at[U];
+      pick(cur.at, k, at);
+      if (lane == 0 && rg == 0 && k < nk) issue(at, it + k);
     }
+    if (nk > kSteps - ST) nxt = lookup(s, 1);
   };
   auto stream_sync = [&]() {
     if constexpr (R == 1) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(1 + stream), "r"(32 * R) : "memory");
   };
 
-  Segment seg;
-  load_group(seg);
-  place(seg);
+  place();
+  bool first_segment = true;
+  int which = 0;
   __syncthreads();  // barriers initialised
   prologue(seg);
-  const int rows = a.G * a.T;
-  bool first_segment = true;
+  if (tid == 0) s_seg[0] = seg;
+  __syncthreads();
 
   for (;;) {
+    const Segment& now = s_seg[which];
     // ---- the unit's queries
-    int qi[NT][2];       // positions of this lane's columns (rows 2·t4, 2·t4 + 1 of each group of 8)
+    int qd[NT][2];  // the lane's columns (rows 2·t4, 2·t4 + 1 of each group of 8): position − reference distance − g
     float slope2[NT][2];
     int2 ref = make_int2(0, 0);
-    if (a.slopes) ref = make_int2(tile_position(a, seg, seg.t0), tile_position(a, seg, seg.t1 - 1) + kTile - 1);
-    int dist0[NT][2];
+    if (a.slopes) ref = make_int2(tile_position(a, now, now.t0), tile_position(a, now, now.t1 - 1) + kTile - 1);
     uint32_t qf[KS][NT][2];
     float qsum[NT][2], qdown[NT][2];  // 4 bits: (Σ q)·factor, factor/2^k of the lane's columns
+    auto row_position = [&](int nt, int e) {
+      const int row = (rg * NT + nt) * 8 + 2 * t4 + e;
+      return now.vis.L - a.T + (row < rows ? row : 0) / a.G;
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int row = (rg * NT + nt) * 8 + 2 * t4 + e, rr = row < rows ? row : 0, t = rr / a.G;
-        qi[nt][e] = seg.vis.L - a.T + t;
         slope2[nt][e] = 0.f;
-        dist0[nt][e] = 0;
+        qd[nt][e] = 0;
         if (a.slopes) {
-          const float sl = a.slopes[seg.h * a.G + rr - t * a.G];
+          const int row = (rg * NT + nt) * 8 + 2 * t4 + e, rr = row < rows ? row : 0;
+          const float sl = a.slopes[now.h * a.G + rr % a.G];
+          const int i = row_position(nt, e);
           slope2[nt][e] = sl * kLog2e;
-          dist0[nt][e] = ref_distance(sl, qi[nt][e], ref);
+          qd[nt][e] = i - ref_distance(sl, i, ref) - g;
         }
       }
-      const int row = (rg * NT + nt) * 8 + g, rr = row < rows ? row : 0, t = rr / a.G;
-      const bf16* qp = a.q + ((static_cast<size_t>(seg.b) * a.T + t) * a.Hq + seg.h * a.G + rr - t * a.G) * D;
       if constexpr (!Q4) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          qf[ks][nt][0] = *reinterpret_cast<const uint32_t*>(qp + 16 * ks + 2 * t4);
-          qf[ks][nt][1] = *reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8 + 2 * t4);
+          qf[ks][nt][0] = q_raw[nt][2 * ks];
+          qf[ks][nt][1] = q_raw[nt][2 * ks + 1];
         }
       } else {
         // fp16, scaled by a power of two to a largest number in [2^14, 2^15): bf16's
         // 8 bits fit, and what falls below fp16's range is under 2^-38 of the
-        // largest.  The k order is that of the codes: word w of lane t4's share
-        // (D/4 numbers from D/4·t4) gives the pairs (8w + i, 8w + i + 4); codes at
-        // odd i come 16 times too large, so their numbers are divided by 16.
-        float x[D / 4], sum = 0.f, top = 0.f;
+        // largest.  Word w of the lane's share gives the pairs (8w + i, 8w + i + 4),
+        // as the codes do; codes at odd i come 16 times too large, so their
+        // numbers are divided by 16.
+        float sum = 0.f, top = 0.f;
 #pragma unroll
-        for (int w = 0; w < D / 32; ++w) load8(qp + D / 4 * t4 + 8 * w, x + 8 * w);
-#pragma unroll
-        for (int i = 0; i < D / 4; ++i) {
-          sum += x[i];
-          top = fmaxf(top, fabsf(x[i]));
+        for (int i = 0; i < D / 8; ++i) {
+          const float lo = bf16_lo(q_raw[nt][i]), hi = bf16_hi(q_raw[nt][i]);
+          sum += lo + hi;
+          top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
         }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int k = min(126, 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23));
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + max(k, -126)) << 23);
+        const int k = 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + max(-126, min(126, k))) << 23);
 #pragma unroll
         for (int w = 0; w < D / 32; ++w)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float by = (i & 1) ? up * 0.0625f : up;
-            const __half2 h = __floats2half2_rn(x[8 * w + i] * by, x[8 * w + i + 4] * by);
+            const uint32_t x = q_raw[nt][4 * w + (i >> 1)], y = q_raw[nt][4 * w + 2 + (i >> 1)];
+            const __half2 h = (i & 1) ? __floats2half2_rn(bf16_hi(x) * by, bf16_hi(y) * by)
+                                      : __floats2half2_rn(bf16_lo(x) * by, bf16_lo(y) * by);
             qf[2 * w + (i >> 1)][nt][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
           }
         const float zf = a.cap2 != 0.f ? a.capx : a.scale2, down = zf / up;
@@ -440,45 +526,40 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
       }
     }
 
-    float o[MT][NT][4], m_sub[NT][2], m_lim[NT][2], l[NT][2], corr[NT][2];
+    float o[MT][NT][4], m[NT][2], l[NT][2], corr[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int j = 0; j < MT; ++j) o[j][nt][0] = o[j][nt][1] = o[j][nt][2] = o[j][nt][3] = 0.f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m_sub[nt][e] = 0.f;         // subtracted from scores: the reference maximum, 0 while there is none
-        m_lim[nt][e] = -INFINITY;   // a score above it moves the reference
+        m[nt][e] = kNoMax;  // the reference maximum
         l[nt][e] = corr[nt][e] = 0.f;
       }
     }
 
     // ---- the tiles
-    const int nk = stream_steps(seg);
-    const int i_first = seg.vis.L - a.T;
+    const int nk = stream_steps(now);
     for (int k = 0; k < nk; ++k, ++it) {
       if (k > 0 && k % kSteps == 0) {
         cur = nxt;
-        nxt = lookup(seg, k / kSteps + 1);
+        nxt = lookup(now, k / kSteps + 1);
       }
-      Tile tl[U];
-      pick(cur, k, tl);
+      int j0[U];
+      pick(cur.j0, k, j0);
       const int sl = it % ST;
       const unsigned int parity = static_cast<unsigned int>(it / ST) & 1u;
       if (!mbar_wait(&my_bar[sl], parity)) mbar_wait(&my_bar[sl], parity);
       unsigned char* const buf = my_ring + sl * Sh::slot_bytes;
-      bool whole = true;
+      int flags = 3;
 #pragma unroll
-      for (int u = 0; u < U; ++u) whole = whole && (tl[u].j0 & 1) != 0;
+      for (int u = 0; u < U; ++u) flags &= j0[u];
+      const bool whole = flags & 1;
 
       // scores: Sᵀ of the step's tiles, in base 2 when there is no cap, else over the cap
       float z[U][NT][4];
       if constexpr (!Q4) {
         float z2[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z[0][nt][e] = z2[nt][e] = 0.f;
         const uint32_t kbase = smem_addr(buf);
         const int tok = lane & 15, ch = lane >> 4;
 #pragma unroll
@@ -487,7 +568,11 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           uint32_t af[4];
           ldsm_x4(kbase + (c >> 3) * (kTile * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4), af);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_bf16(ks & 1 ? z2[nt] : z[0][nt], af, qf[ks][nt][0], qf[ks][nt][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            float(&to)[4] = ks & 1 ? z2[nt] : z[0][nt];
+            if (ks < 2) mma_first<false>(to, af, qf[ks][nt]);
+            else mma<false>(to, af, qf[ks][nt], to);
+          }
         }
         const float zf = a.cap2 != 0.f ? a.capx : a.scale2;
 #pragma unroll
@@ -498,11 +583,6 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const unsigned char* rec = buf + u * (Sh::slot_bytes / U);
-          float z2[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[u][nt][e] = z2[nt][e] = 0.f;
           uint32_t w0[D / 32], w1[D / 32];
           const unsigned char* k0 = rec + g * (D / 2) + t4 * (D / 8);
           if constexpr (D == 128) {
@@ -523,17 +603,18 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
               const uint32_t x = w0[w] >> (8 * b), y = w1[w] >> (8 * b);
               const uint32_t af[4] = {q4_half_low(x), q4_half_low(y), q4_half_high(x), q4_half_high(y)};
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(b ? z2[nt] : z[u][nt], af, qf[2 * w + b][nt][0], qf[2 * w + b][nt][1]);
+              for (int nt = 0; nt < NT; ++nt) {
+                if (w + b == 0) mma_first<true>(z[u][nt], af, qf[0][nt]);
+                else mma<true>(z[u][nt], af, qf[2 * w + b][nt], z[u][nt]);
+              }
             }
-          const float ks0 = bf16_lo(ka), ks1 = bf16_lo(kb);
-          const float km0 = fmaf(8.f, ks0, bf16_hi(ka)), km1 = fmaf(8.f, ks1, bf16_hi(kb));
+          const float ks0 = bf16_lo(ka), ks1 = bf16_lo(kb), kz0 = bf16_hi(ka), kz1 = bf16_hi(kb);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              z[u][nt][e] = fmaf(ks0, (z[u][nt][e] + z2[nt][e]) * qdown[nt][e], km0 * qsum[nt][e]);
-              z[u][nt][2 + e] = fmaf(ks1, (z[u][nt][2 + e] + z2[nt][2 + e]) * qdown[nt][e], km1 * qsum[nt][e]);
+              z[u][nt][e] = fmaf(ks0, z[u][nt][e] * qdown[nt][e], kz0 * qsum[nt][e]);
+              z[u][nt][2 + e] = fmaf(ks1, z[u][nt][2 + e] * qdown[nt][e], kz1 * qsum[nt][e]);
             }
         }
       }
@@ -552,14 +633,15 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int far = qi[nt][e] - (tl[u].j0 & -kTile), near = far - 15;
-              if (near >= 0) {  // the whole tile lies behind the query: the bias is linear
-                const float at = static_cast<float>(far - dist0[nt][e]) - static_cast<float>(g);
+              const int first = j0[u] & -kTile;
+              if (flags & 2) {  // behind the query the bias is linear
+                const float at = static_cast<float>(qd[nt][e] - first);
                 z[u][nt][e] = fmaf(-slope2[nt][e], at, z[u][nt][e]);
                 z[u][nt][2 + e] = fmaf(-slope2[nt][e], at - 8.f, z[u][nt][2 + e]);
               } else {
-                z[u][nt][e] = fmaf(-slope2[nt][e], static_cast<float>(abs(far - g) - dist0[nt][e]), z[u][nt][e]);
-                z[u][nt][2 + e] = fmaf(-slope2[nt][e], static_cast<float>(abs(far - g - 8) - dist0[nt][e]), z[u][nt][2 + e]);
+                const int i = row_position(nt, e), d0 = i - g - qd[nt][e], off = i - first - g;
+                z[u][nt][e] = fmaf(-slope2[nt][e], static_cast<float>(abs(off) - d0), z[u][nt][e]);
+                z[u][nt][2 + e] = fmaf(-slope2[nt][e], static_cast<float>(abs(off - 8) - d0), z[u][nt][2 + e]);
               }
             }
       }
@@ -567,8 +649,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
       uint32_t apart = 0;  // bf16: tokens that some rows see and others do not, with a V that is not finite
       if (!whole) {
         auto sees = [&](int i, int j) {
-          return j >= seg.vis.start && i >= 0 && j < seg.vis.L &&
-                 (j < seg.vis.prefix || (j <= i && (a.window <= 0 || i - j < a.window)));
+          return j >= now.vis.start && i >= 0 && j < now.vis.L &&
+                 (j < now.vis.prefix || (j <= i && (a.window <= 0 || i - j < a.window)));
         };
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -576,14 +658,14 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (!sees(qi[nt][e & 1], (tl[u].j0 & -kTile) + g + (e >> 1) * 8)) z[u][nt][e] = -INFINITY;
+              if (!sees(row_position(nt, e & 1), (j0[u] & -kTile) + g + (e >> 1) * 8)) z[u][nt][e] = -INFINITY;
         if constexpr (!Q4) {
           // 0·V must not turn a masked NaN into the sum: rows of V that nobody
           // sees are zeroed; a row only some see is set apart if it has one
           bool any = false, all = true;
           if (lane < kTile)
             for (int t = 0; t < a.T; ++t) {
-              const bool v = sees(i_first + t, (tl[0].j0 & -kTile) + lane);
+              const bool v = sees(now.vis.L - a.T + t, (j0[0] & -kTile) + lane);
               any |= v;
               all &= v;
             }
@@ -614,11 +696,11 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
       // a score far above the reference: new maxima, and the state follows
       bool grow = false;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) grow |= z[u][nt][e] > m_lim[nt][e & 1];
+          for (int u = 0; u < U; ++u) grow |= z[u][nt][e] > m[nt][e & 1] + kGrow;
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -629,11 +711,9 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float old = m_lim[nt][e] - kGrow;  // −inf at first
-            if (top > old) {
-              const float f = ex2(old - top);
-              m_sub[nt][e] = top;
-              m_lim[nt][e] = top + kGrow;
+            if (top > m[nt][e]) {
+              const float f = ex2(m[nt][e] - top);
+              m[nt][e] = top;
               l[nt][e] *= f;
               corr[nt][e] *= f;
 #pragma unroll
@@ -662,7 +742,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            p[e] = ex2(z[u][nt][e] - m_sub[nt][e & 1]);
+            p[e] = ex2(z[u][nt][e] - m[nt][e & 1]);
             l[nt][e & 1] += p[e];
           }
           if constexpr (!Q4) {
@@ -731,19 +811,31 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
       if constexpr (!Q4) {
         const uint32_t vbase = smem_addr(buf) + D / 64 * kTile * 128;
         const int tok = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
+        constexpr int JB = NT == 1 ? 4 : 2;  // independent products in flight: JB·NT
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          const int c = 2 * j + ch;
-          uint32_t af[4];
-          ldsm_x4_trans(vbase + (c >> 3) * (kTile * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4), af);
+        for (int j0v = 0; j0v < MT; j0v += JB) {
+          uint32_t af[JB][4];
+          float t[JB][NT][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float t[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int part = 2; part >= 0; --part) mma_bf16(t, af, pf[0][nt][part][0], pf[0][nt][part][1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][nt][e] += t[e];
+          for (int jj = 0; jj < JB; ++jj) {
+            const int c = 2 * (j0v + jj) + ch;
+            ldsm_x4_trans(vbase + (c >> 3) * (kTile * 128) + tok * 128 + (((c & 7) ^ (tok & 7)) << 4), af[jj]);
           }
+#pragma unroll
+          for (int part = 2; part >= 0; --part)
+#pragma unroll
+            for (int jj = 0; jj < JB; ++jj)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                if (part == 2) mma_first<false>(t[jj][nt], af[jj], pf[0][nt][part]);
+                else mma<false>(t[jj][nt], af[jj], pf[0][nt][part], t[jj][nt]);
+              }
+#pragma unroll
+          for (int jj = 0; jj < JB; ++jj)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[j0v + jj][nt][e] += t[jj][nt][e];
         }
       } else {
         // The codes enter as 16 + n (no subtraction): products with the first
@@ -754,9 +846,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
         const uint32_t m24[4] = {0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          c24[nt][0] = c24[nt][1] = c24[nt][2] = c24[nt][3] = 0.f;
-#pragma unroll
-          for (int u = 0; u < U; ++u) mma_bf16(c24[nt], m24, pf[u][nt][0][0], pf[u][nt][0][1]);
+          mma_first<false>(c24[nt], m24, pf[0][nt][0]);
+          if constexpr (U == 2) mma<false>(c24[nt], m24, pf[U - 1][nt][0], c24[nt]);
         }
         // lane (g, t4): tokens 2·t4, 2·t4 + 1 (+ 8), numbers D/8·g … of each;
         // the byte interleave pairs the two tokens' codes of one number
@@ -785,52 +876,68 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
               un[u][hf][2 * w + 1] = __byte_perm(wv[2 * hf][w], wv[2 * hf + 1][w], 0x7632);
             }
         }
+        constexpr int JB = 2;  // independent products in flight: JB·NT
 #pragma unroll
-        for (int j = 0; j < MT; ++j) {
-          // m rows g: number j of the lane's share; rows g + 8: number MT + j
-          uint32_t af[U][4];
+        for (int j0v = 0; j0v < MT; j0v += JB) {
+          uint32_t af[U][JB][4];
+          float t[JB][NT][4];
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            af[u][0] = q4_pair16(un[u][0][j / 4], j & 3);
-            af[u][1] = q4_pair16(un[u][0][MT / 4 + j / 4], j & 3);
-            af[u][2] = q4_pair16(un[u][1][j / 4], j & 3);
-            af[u][3] = q4_pair16(un[u][1][MT / 4 + j / 4], j & 3);
-          }
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float t[4] = {c24[nt][0], c24[nt][1], c24[nt][2], c24[nt][3]};
+            for (int jj = 0; jj < JB; ++jj) {
+              // m rows g: number j of the lane's share; rows g + 8: number MT + j
+              const int j = j0v + jj;
+              af[u][jj][0] = q4_pair16(un[u][0][j / 4], j & 3);
+              af[u][jj][1] = q4_pair16(un[u][0][MT / 4 + j / 4], j & 3);
+              af[u][jj][2] = q4_pair16(un[u][1][j / 4], j & 3);
+              af[u][jj][3] = q4_pair16(un[u][1][MT / 4 + j / 4], j & 3);
+            }
 #pragma unroll
-            for (int part = 0; part < 3; ++part)
+          for (int part = 0; part < 3; ++part)
 #pragma unroll
-              for (int u = 0; u < U; ++u) mma_bf16(t, af[u], pf[u][nt][part][0], pf[u][nt][part][1]);
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][nt][e] += t[e];
-          }
+              for (int jj = 0; jj < JB; ++jj)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (part == 0 && u == 0) mma<false>(t[jj][nt], af[u][jj], pf[u][nt][part], c24[nt]);
+                  else mma<false>(t[jj][nt], af[u][jj], pf[u][nt][part], t[jj][nt]);
+                }
+#pragma unroll
+          for (int jj = 0; jj < JB; ++jj)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[j0v + jj][nt][e] += t[jj][nt][e];
         }
       }
       // the slot is free: the next copies into it
       stream_sync();
       const int ahead = k + ST;
-      Tile x[U];
-      pick(ahead / kSteps == k / kSteps ? cur : nxt, ahead, x);
+      int at[U];
+      pick(ahead / kSteps == k / kSteps ? cur.at : nxt.at, ahead, at);
       if (lane == 0 && rg == 0 && ahead < nk) {
         fence_proxy_async_shared();  // the slot's reads come before the copies that refill it
-        issue(x, it + ST);
+        issue(at, it + ST);
       }
     }
 
     // ---- the next unit's copies start before this one's warps are added up
-    const Segment done = seg;
-    pos += seg.t1 - seg.t0;
-    const bool more = pos < end;
-    if (more) {
-      if (pos >= grp_at + static_cast<long long>(seg.n) * mult) {
-        grp_at += static_cast<long long>(seg.n) * mult;
-        ++grp;
-        load_group(seg);
+    bool more = false;
+    if (!aligned) {
+      pos += now.t1 - now.t0;
+      more = pos < end;
+      if (more) {
+        if (pos >= grp_at + static_cast<long long>(seg.n) * mult) {
+          grp_at += static_cast<long long>(seg.n) * mult;
+          ++grp;
+          seg.n = group_tiles(a, grp);
+          seg.vis = visible_tiles(a, a.sel ? grp / a.Hkv : grp);
+        }
+        place();
+        prologue(seg);
+        if (tid == 0) s_seg[which ^ 1] = seg;
       }
-      place(seg);
-      prologue(seg);
     }
 
 #pragma unroll
@@ -843,7 +950,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           if constexpr (Q4) corr[nt][e] += __shfl_xor_sync(0xffffffffu, corr[nt][e], sh);
         }
         if (g == 0) {
-          s_m[warp][nt * 8 + 2 * t4 + e] = m_lim[nt][e] - kGrow;
+          s_m[warp][nt * 8 + 2 * t4 + e] = m[nt][e] == kNoMax ? -INFINITY : m[nt][e];
           s_l[warp][nt * 8 + 2 * t4 + e] = l[nt][e];
           s_c[warp][nt * 8 + 2 * t4 + e] = corr[nt][e];
         }
@@ -866,7 +973,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
         }
       }
     __syncthreads();
-    const bool entire = done.t0 == 0 && done.t1 == done.n;
+    const bool entire = now.t0 == 0 && now.t1 == now.n;
     const int slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
     for (int i = tid; i < rows * (D / 4); i += Sh::threads) {
       const int row = i / (D / 4), c = (i - row * (D / 4)) * 4, r = row / (8 * NT), in = row - r * (8 * NT);
@@ -894,8 +1001,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
         sum.w += cc;
       }
       if (entire) {
-        const int t = row / a.G, hq = done.h * a.G + row - t * a.G;
-        const size_t orow = (static_cast<size_t>(done.b) * a.T + t) * a.Hq + hq;
+        const int t = row / a.G, hq = now.h * a.G + row - t * a.G;
+        const size_t orow = (static_cast<size_t>(now.b) * a.T + t) * a.Hq + hq;
         const bool none = top == -INFINITY && den == den;  // no visible token with a score above −inf
         const float by = none ? 0.f : 1.f / den;
         *reinterpret_cast<float4*>(a.out + orow * D + c) =
@@ -904,7 +1011,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           float lse = none ? -INFINITY : (top + log2f(den)) * kLn2;
           if (a.slopes && !none) {
             const float sl = a.slopes[hq];
-            lse -= sl * static_cast<float>(ref_distance(sl, done.vis.L - a.T + t, ref));
+            lse -= sl * static_cast<float>(ref_distance(sl, now.vis.L - a.T + t, ref));
           }
           a.lse[orow] = lse;
         }
@@ -915,66 +1022,76 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
     }
     if (!entire && tid == 0) {
       a.ref[slot] = ref;
-      if (done.t0 == 0) {  // the unit's first piece: CTAs that hold the others follow
-        const long long last = pos - (done.t1 - done.t0) + done.n - 1;
-        a.cut[blockIdx.x] = make_int4(done.unit, slot, static_cast<int>(last / per) - static_cast<int>(blockIdx.x) + 1, 0);
-      }
+      // the unit's first piece: the CTAs that follow hold the others
+      if (now.t0 == 0) a.cut[blockIdx.x] = make_int4(now.unit, slot, now.pieces, 0);
     }
     if (!more) return;
     first_segment = false;
     __syncthreads();
+    which ^= 1;
   }
 }
 
 // grid (CTAs of mod_kernel, rows), D threads × 4 slices of the pieces: adds the
-// pieces of the unit that CTA x cut, in CTA order.
+// pieces of the unit that CTA x cut, in CTA order.  What bounds it is the chain
+// of dependent loads, so the first pieces are read before their weights are known.
 template <int D>
 __global__ void __launch_bounds__(4 * D) mod_combine_kernel(ModArgs a) {
   grid_dep_enter();
   const int4 cut = a.cut[blockIdx.x];
-  if (cut.z == 0) return;
-  __shared__ float s_num[4][D], s_den[4];
-  const int rows = a.G * a.T, row = blockIdx.y, c = threadIdx.x % D, sl = threadIdx.x / D;
+  if (cut.z <= 1) return;
+  constexpr int kAhead = 8;
+  __shared__ float s_num[4][D];
+  const int rows = a.G * a.T, row = blockIdx.y, c = threadIdx.x % D, sl = threadIdx.x / D, lane = threadIdx.x & 31;
   const int b = cut.x / a.Hkv, h = cut.x - b * a.Hkv, t = row / a.G, hq = h * a.G + row - t * a.G;
   const int cta = blockIdx.x, n = cut.z;
   auto slot = [&](int p) { return static_cast<size_t>(p == 0 ? cut.y : 2 * (cta + p)); };
+  float early[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) early[i] = a.part[(slot(min(sl + 4 * i, n - 1)) * rows + row) * D + c];
   float slope = 0.f;
-  int i = 0;
+  int qpos = 0;
   if (a.slopes) {
     slope = a.slopes[hq];
-    int L = a.seq_lens[b];
-    const int most = a.max_pages * a.S;
-    L = L < 0 ? 0 : (L > most ? most : L);
-    i = L - a.T + t;
+    const int L = a.seq_lens[b], most = a.max_pages * a.S;
+    qpos = (L < 0 ? 0 : (L > most ? most : L)) - a.T + t;
   }
   // the pieces' biases are measured from distances of their own: all to the
   // last piece's (the nearest tokens), or the first's for a rising bias
-  const int base = a.slopes ? ref_distance(slope, i, a.ref[slot(slope >= 0.f ? n - 1 : 0)]) : 0;
-  auto top_of = [&](int p) {
-    const float m = a.ml[slot(p) * rows + row].x;
-    return a.slopes ? m - slope * kLog2e * static_cast<float>(ref_distance(slope, i, a.ref[slot(p)]) - base) : m;
+  const int base = a.slopes ? ref_distance(slope, qpos, a.ref[slot(slope >= 0.f ? n - 1 : 0)]) : 0;
+  auto top_of = [&](int p, float m) {
+    return a.slopes ? m - slope * kLog2e * static_cast<float>(ref_distance(slope, qpos, a.ref[slot(p)]) - base) : m;
   };
-  float top = -INFINITY;
-  for (int p = threadIdx.x & 31; p < n; p += 32) top = fmaxf(top, top_of(p));
-  top = warp_max(top);
-  float num = 0.f, den = 0.f;
-#pragma unroll 4
-  for (int p = sl; p < n; p += 4) {
-    const float m = top_of(p), f = m > -INFINITY ? ex2(m - top) : 0.f;
-    num = fmaf(a.part[(slot(p) * rows + row) * D + c], f, num);
-    den = fmaf(a.ml[slot(p) * rows + row].y, f, den);
+  // every warp: all pieces' maxima and sums, one piece per lane
+  float top = -INFINITY, den = 0.f;
+  for (int p = lane; p < n; p += 32) {
+    const float2 x = a.ml[slot(p) * rows + row];
+    const float m = top_of(p, x.x), up = fmaxf(top, m);
+    if (up > -INFINITY) den = den * ex2(top - up) + x.y * ex2(m - up);
+    else den += x.y;
+    top = up;
   }
+  const float all = warp_max(top);
+  den = warp_sum(all > -INFINITY ? den * ex2(top - all) : den);
+  float num = 0.f;
+  auto add = [&](int p, float x) {
+    const float m = top_of(p, a.ml[slot(p) * rows + row].x);
+    num = fmaf(x, m > -INFINITY ? ex2(m - all) : 0.f, num);
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (sl + 4 * i < n) add(sl + 4 * i, early[i]);
+#pragma unroll 4
+  for (int p = sl + 4 * kAhead; p < n; p += 4) add(p, a.part[(slot(p) * rows + row) * D + c]);
   s_num[sl][c] = num;
-  if (c == 0) s_den[sl] = den;
   __syncthreads();
   if (sl != 0) return;
   num = s_num[0][c] + s_num[1][c] + s_num[2][c] + s_num[3][c];
-  den = s_den[0] + s_den[1] + s_den[2] + s_den[3];
   const size_t orow = (static_cast<size_t>(b) * a.T + t) * a.Hq + hq;
-  const bool none = top == -INFINITY && den == den;
+  const bool none = all == -INFINITY && den == den;
   a.out[orow * D + c] = none ? 0.f : num / den;
   if (c == 0 && a.lse)
-    a.lse[orow] = none ? -INFINITY : (top + log2f(den)) * kLn2 - slope * static_cast<float>(base);
+    a.lse[orow] = none ? -INFINITY : (all + log2f(den)) * kLn2 - slope * static_cast<float>(base);
 }
 
 // Two-dimensional view [rows, d] of a pool, copied 16 rows × 64 columns at a
@@ -1054,6 +1171,7 @@ cudaError_t launch_softmax_mod(const ekv_cache& c, const void* pool, const ekv_s
   a.max_pages = s.max_pages;
   a.cap = cap;
   a.min_tiles = 8;
+  a.slack_tiles = pool ? 32 : 12;
   a.scale2 = scale * kLog2e;
   if (mod != nullptr) {
     a.slopes = mod->slopes;
