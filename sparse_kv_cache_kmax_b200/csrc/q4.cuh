@@ -41,18 +41,6 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t b
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w), "r"(mask), "r"(bits));
   return x;
 }
-// The codes at bits 0..3 of each half of w as an fp16 pair n, and those at bits
-// 4..7 as 16·n, exactly: 0x6400 | x is 1024 + x in fp16.
-__device__ __forceinline__ uint32_t q4_half_low(uint32_t w) {
-  const uint32_t x = and_or(w, 0x000f000fu, 0x64006400u);
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6400)));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t q4_half_high(uint32_t w) {
-  const uint32_t x = and_or(w, 0x00f000f0u, 0x64006400u);
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6400)));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 // The codes at bits 4i..4i+3 of each half of w as a bf16 pair 16 + n: 0x4180 | n << 3.
 __device__ __forceinline__ uint32_t q4_pair16(uint32_t w, int i) {
   return and_or(i == 0 ? w << 3 : w >> (4 * i - 3), 0x00780078u, 0x41804180u);

@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
                                       : __floats2half2_rn(bf16_lo(x) * by, bf16_lo(y) * by);
             qf[2 * w + (i >> 1)][nt][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
           }
-        const float zf = a.cap2 != 0.f ? a.capx : a.scale2, down = zf / up;
+        const float zf = a.cap2 != 0.f ? a.capx : a.scale2, down = zf / up * 16777216.f;
         qsum[nt][0] = __shfl_sync(0xffffffffu, sum * zf, 8 * t4);
         qsum[nt][1] = __shfl_sync(0xffffffffu, sum * zf, 8 * t4 + 4);
         qdown[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t4);
@@ -600,8 +600,11 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           for (int w = 0; w < D / 32; ++w)
 #pragma unroll
             for (int b = 0; b < 2; ++b) {  // codes 0, 1, 4, 5 of a word, then 2, 3, 6, 7
+              // As fp16, 0x000n is the subnormal n·2⁻²⁴ and 0x00n0 is 16n·2⁻²⁴: a code
+              // in the low byte of a half is a number already (the tensor cores take
+              // subnormals exactly).
               const uint32_t x = w0[w] >> (8 * b), y = w1[w] >> (8 * b);
-              const uint32_t af[4] = {q4_half_low(x), q4_half_low(y), q4_half_high(x), q4_half_high(y)};
+              const uint32_t af[4] = {x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 if (w + b == 0) mma_first<true>(z[u][nt], af, qf[0][nt]);
