@@ -9,8 +9,6 @@
 // tokens is one contiguous block (2176 B at d = 128), so one bulk copy brings it.
 #pragma once
 
-#include <cuda_fp16.h>
-
 #include "kernels.cuh"
 
 namespace ekv {
@@ -33,17 +31,6 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // The value a code stands for: zero + step·n, rounded once to fp32.
 __device__ __forceinline__ float q4_value(uint32_t step_zero, uint32_t n) {
   return fmaf(bf16_lo(step_zero), static_cast<float>(n), bf16_hi(step_zero));
-}
-
-// (w & mask) | bits in one instruction.
-__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
-  uint32_t x;
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(x) : "r"(w), "r"(mask), "r"(bits));
-  return x;
-}
-// The codes at bits 4i..4i+3 of each half of w as a bf16 pair 16 + n: 0x4180 | n << 3.
-__device__ __forceinline__ uint32_t q4_pair16(uint32_t w, int i) {
-  return and_or(i == 0 ? w << 3 : w >> (4 * i - 3), 0x00780078u, 0x41804180u);
 }
 
 }  // namespace ekv

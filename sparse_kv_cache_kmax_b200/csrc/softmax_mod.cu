@@ -24,6 +24,7 @@
 //
 // The bound is HBM: 512 bytes per bf16 (token, KV head), 136 in 4 bits.
 #include <cuda.h>
+#include <cuda_fp16.h>
 
 #include "q4.cuh"
 
@@ -177,7 +178,7 @@ struct Tile {
 
 __device__ __forceinline__ Tile resolve_tile(const ModArgs& a, const Segment& s, int t) {
   Tile r{-1, -kTile};
-  if (t >= s.t1 || s.vis.n == 0) return r;
+  if (t < s.t0 || s.vis.n == 0) return r;
   const int tpp = a.S / kTile;
   int lp, part;
   if (a.sel == nullptr) {
@@ -242,11 +243,20 @@ struct Shape {
   static constexpr int threads = 32 * NW;
 };
 
+// Floats from one row of the merge buffer to the next, and where number d of a
+// row lies: 2·pitch is 8 or 24 mod 32, and the 4-bit lanes' shares of D/8
+// numbers are one apart, so that the warps' stores meet no bank twice.
+constexpr int merge_pitch(int d, bool q4) { return q4 ? d + 12 : d + 4; }
+template <int D, bool Q4>
+__device__ __forceinline__ int merge_at(int d) {
+  return Q4 ? d + d / (D / 8) : d;
+}
+
 template <int D, int NT, int R, bool Q4>
 constexpr int mod_stages() {
   // as many copies in flight as two CTAs' shared memory holds beside the merge buffer
   using Sh = Shape<D, NT, Q4>;
-  constexpr int merge = (Sh::NW * 8 * NT) * (D + 4) * 4;
+  constexpr int merge = (Sh::NW * 8 * NT) * merge_pitch(D, Q4) * 4;
   constexpr int room = 112 * 1024 - merge;
   constexpr int n = room / (Sh::NW / R * Sh::slot_bytes);
   return n > 6 ? 6 : n;
@@ -256,7 +266,7 @@ template <int D, int NT, int R, bool Q4>
 constexpr size_t mod_smem() {
   using Sh = Shape<D, NT, Q4>;
   return 1024 + static_cast<size_t>(Sh::NW / R) * mod_stages<D, NT, R, Q4>() * Sh::slot_bytes +
-         static_cast<size_t>(Sh::NW * 8 * NT) * (D + 4) * 4;
+         static_cast<size_t>(Sh::NW * 8 * NT) * merge_pitch(D, Q4) * 4;
 }
 
 // R: warps that share a tile stream, each with its own rows (8·NT·R ≥ G·T).
@@ -265,17 +275,14 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
     mod_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, ModArgs a) {
   using Sh = Shape<D, NT, Q4>;
   constexpr int NW = Sh::NW, U = Sh::U, NS = NW / R, ST = mod_stages<D, NT, R, Q4>();
-  constexpr int KS = D / 16, MT = D / 16, PITCH = D + 4;
+  constexpr int KS = D / 16, MT = D / 16, PITCH = merge_pitch(D, Q4);
   static_assert(ST >= 2 && NW % R == 0, "ring too small");
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t bars[NS * ST];
   __shared__ float s_m[NW][8 * NT], s_l[NW][8 * NT], s_c[NW][8 * NT];
-  __shared__ int scan_s[33];
+  constexpr bool kSharedQ = Q4 && NT == 1;  // one set of query fragments for all warps, to spare registers
+  __shared__ uint2 s_q[kSharedQ ? KS : 1][32];
   __shared__ Segment s_seg[2];  // the unit in work, and the next
-  __shared__ struct {
-    long long at;  // start of the group in the list
-    int grp, tiles;
-  } s_found;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int stream = warp / R, rg = warp - stream * R;
@@ -291,17 +298,26 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   // This CTA's run of the work list.  Cutting the list into equal runs keeps
   // every CTA equally busy but lets one cross units, which costs it a second
   // set of queries and a second merge; cutting every unit into equal pieces
-  // costs nothing while there are CTAs enough, so that comes first.
+  // costs nothing while there are CTAs enough, so that comes first.  Every warp
+  // works it out by itself, four groups per lane at a time: block-wide scans
+  // cost four times as long (2.4 us of a 24 us call).
   const int mult = a.sel ? 1 : a.Hkv, groups = a.sel ? a.batch * a.Hkv : a.batch;
-  const int mine0 = tid < groups ? group_tiles(a, tid) : 0;  // most batches: one group per thread
-  auto tiles_of = [&](int c0) { return c0 == 0 ? mine0 : (c0 + tid < groups ? group_tiles(a, c0 + tid) : 0); };
+  int mine[4];  // tiles of groups 4·lane .. + 3 of the chunk in work
+  int held = -1;
+  auto load_chunk = [&](int c0) {
+    if (held == c0) return;
+    held = c0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mine[i] = c0 + 4 * lane + i < groups ? group_tiles(a, c0 + 4 * lane + i) : 0;
+  };
   auto sum_over_groups = [&](auto value) {  // value(tiles), times the units of a group
     long long total = 0;
-    for (int c0 = 0; c0 < groups; c0 += Sh::threads) {
-      int sum;
-      block_exclusive_scan(value(tiles_of(c0)) * mult, scan_s, &sum);
-      total += sum;
-      __syncthreads();
+    for (int c0 = 0; c0 < groups; c0 += 128) {
+      load_chunk(c0);
+      int x = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x += value(mine[i]);
+      total += static_cast<long long>(warp_sum(x)) * mult;
     }
     return total;
   };
@@ -321,34 +337,52 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
       }
     }
   }
+  if (tid == 0) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
   // the group that holds this CTA's start: counted in pieces, or in tiles
   const long long start = aligned ? blockIdx.x : static_cast<long long>(per) * blockIdx.x;
-  long long pos = start, before = 0;
-  if (tid == 0) {
-    a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
-    s_found.grp = -1;
-  }
-  __syncthreads();
-  for (int c0 = 0; c0 < groups && before <= start; c0 += Sh::threads) {
-    int sum;
-    const int n = tiles_of(c0), mine = (aligned ? (n + per - 1) / per : n) * mult;
-    const int ex = block_exclusive_scan(mine, scan_s, &sum);
-    if (before + ex <= start && start < before + ex + mine) {
-      s_found.at = before + ex;
-      s_found.grp = c0 + tid;
-      s_found.tiles = n;
+  long long pos = start, grp_at = 0;
+  int grp = -1, grp_tiles = 0;
+  for (int c0 = 0; c0 < groups && grp < 0; c0 += 128) {
+    load_chunk(c0);
+    int len[4], x = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      len[i] = (aligned ? (mine[i] + per - 1) / per : mine[i]) * mult;
+      x += len[i];
     }
-    before += sum;
-    __syncthreads();
+    int up = x;  // inclusive scan over the lanes
+#pragma unroll
+    for (int sh = 1; sh < 32; sh <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, up, sh);
+      if (lane >= sh) up += y;
+    }
+    const int off = start - grp_at < 0x7fffffff ? static_cast<int>(start - grp_at) : 0x7fffffff;
+    int at = up - x, which = -1, tiles = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (which < 0 && at <= off && off < at + len[i]) {
+        which = 4 * lane + i;
+        tiles = mine[i];
+      } else if (which < 0) {
+        at += len[i];
+      }
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, which >= 0);
+    if (hit) {
+      const int from = __ffs(hit) - 1;
+      grp = c0 + __shfl_sync(0xffffffffu, which, from);
+      grp_tiles = __shfl_sync(0xffffffffu, tiles, from);
+      grp_at += __shfl_sync(0xffffffffu, at, from);
+    } else {
+      grp_at += __shfl_sync(0xffffffffu, up, 31);
+    }
   }
-  int grp = s_found.grp;
   if (grp < 0) return;  // more CTAs than runs
-  long long grp_at = s_found.at;
   const long long end = pos + per < total ? pos + per : total;  // of a run of tiles
 
   Segment seg;  // the next one to work on; s_seg holds the one in work
   seg.vis = visible_tiles(a, a.sel ? grp / a.Hkv : grp);
-  seg.n = s_found.tiles;
+  seg.n = grp_tiles;
   auto place = [&]() {  // the unit at pos of group grp
     const int off = static_cast<int>(pos - grp_at);
     seg.b = a.sel ? grp / a.Hkv : grp;
@@ -396,15 +430,18 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
       }
     }
   };
-  // A stream's step k is tiles t0 + U·(stream + NS·k) .. + U − 1; a lookup
-  // resolves the 32 tiles of 32/U steps, one per lane.
+  // A stream's step k is tiles U·(stream + NS·k) .. + U − 1 of the segment, counted
+  // from its end: under a bias that falls with distance the nearest tokens hold
+  // the largest scores, and the reference maximum then hardly ever moves (from the
+  // other end it moved at 62% of all steps).  A lookup resolves the 32 tiles of
+  // 32/U steps, one per lane.
   constexpr int kSteps = 32 / U;
   auto stream_steps = [&](const Segment& s) {
     const int n = s.t1 - s.t0 - U * stream;
     return n > 0 ? (n + U * NS - 1) / (U * NS) : 0;
   };
   auto lookup = [&](const Segment& s, int batch) {
-    return resolve_tile(a, s, s.t0 + U * (stream + NS * (kSteps * batch + lane / U)) + lane % U);
+    return resolve_tile(a, s, s.t1 - 1 - (U * (stream + NS * (kSteps * batch + lane / U)) + lane % U));
   };
   auto pick = [&](int x, int k, int (&to)[U]) {
 #pragma unroll
@@ -463,8 +500,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
     float slope2[NT][2];
     int2 ref = make_int2(0, 0);
     if (a.slopes) ref = make_int2(tile_position(a, now, now.t0), tile_position(a, now, now.t1 - 1) + kTile - 1);
-    uint32_t qf[KS][NT][2];
-    float qsum[NT][2], qdown[NT][2];  // 4 bits: (Σ q)·factor, factor/2^k of the lane's columns
+    uint32_t qf[kSharedQ ? 1 : KS][NT][2];
+    float qsum[NT][2], qdown[NT][2], qc[NT][2];  // 4 bits, the lane's columns: (Σ q)·factor, factor/2^k, −8·Σ q·2^k
     auto row_position = [&](int nt, int e) {
       const int row = (rg * NT + nt) * 8 + 2 * t4 + e;
       return now.vis.L - a.T + (row < rows ? row : 0) / a.G;
@@ -508,6 +545,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int k = 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + max(-126, min(126, k))) << 23);
+        uint32_t qh[KS][2];
 #pragma unroll
         for (int w = 0; w < D / 32; ++w)
 #pragma unroll
@@ -516,11 +554,23 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
             const uint32_t x = q_raw[nt][4 * w + (i >> 1)], y = q_raw[nt][4 * w + 2 + (i >> 1)];
             const __half2 h = (i & 1) ? __floats2half2_rn(bf16_hi(x) * by, bf16_hi(y) * by)
                                       : __floats2half2_rn(bf16_lo(x) * by, bf16_lo(y) * by);
-            qf[2 * w + (i >> 1)][nt][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
+            qh[2 * w + (i >> 1)][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
           }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          if constexpr (kSharedQ) {
+            if (warp == 0) s_q[ks][lane] = make_uint2(qh[ks][0], qh[ks][1]);
+          } else {
+            qf[ks][nt][0] = qh[ks][0];
+            qf[ks][nt][1] = qh[ks][1];
+          }
+        }
         const float zf = a.cap2 != 0.f ? a.capx : a.scale2, down = zf / up * 16777216.f;
         qsum[nt][0] = __shfl_sync(0xffffffffu, sum * zf, 8 * t4);
         qsum[nt][1] = __shfl_sync(0xffffffffu, sum * zf, 8 * t4 + 4);
+        const float c8 = sum * up * -0x1p-21f;
+        qc[nt][0] = __shfl_sync(0xffffffffu, c8, 8 * t4);
+        qc[nt][1] = __shfl_sync(0xffffffffu, c8, 8 * t4 + 4);
         qdown[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t4);
         qdown[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t4 + 4);
       }
@@ -537,6 +587,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
         l[nt][e] = corr[nt][e] = 0.f;
       }
     }
+
+    if constexpr (kSharedQ) __syncthreads();
 
     // ---- the tiles
     const int nk = stream_steps(now);
@@ -580,38 +632,57 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
 #pragma unroll
           for (int e = 0; e < 4; ++e) z[0][nt][e] = (z[0][nt][e] + z2[nt][e]) * zf;
       } else {
+        uint32_t w0[U][D / 32], w1[U][D / 32];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const unsigned char* rec = buf + u * (Sh::slot_bytes / U);
-          uint32_t w0[D / 32], w1[D / 32];
-          const unsigned char* k0 = rec + g * (D / 2) + t4 * (D / 8);
+          const unsigned char* k0 = buf + u * (Sh::slot_bytes / U) + g * (D / 2) + t4 * (D / 8);
           if constexpr (D == 128) {
             const uint4 x = *reinterpret_cast<const uint4*>(k0), y = *reinterpret_cast<const uint4*>(k0 + 8 * (D / 2));
-            w0[0] = x.x; w0[1] = x.y; w0[2] = x.z; w0[3] = x.w;
-            w1[0] = y.x; w1[1] = y.y; w1[2] = y.z; w1[3] = y.w;
+            w0[u][0] = x.x; w0[u][1] = x.y; w0[u][2] = x.z; w0[u][3] = x.w;
+            w1[u][0] = y.x; w1[u][1] = y.y; w1[u][2] = y.z; w1[u][3] = y.w;
           } else {
             const uint2 x = *reinterpret_cast<const uint2*>(k0), y = *reinterpret_cast<const uint2*>(k0 + 8 * (D / 2));
-            w0[0] = x.x; w0[1] = x.y;
-            w1[0] = y.x; w1[1] = y.y;
+            w0[u][0] = x.x; w0[u][1] = x.y;
+            w1[u][0] = y.x; w1[u][1] = y.y;
           }
-          const uint32_t* pairs = reinterpret_cast<const uint32_t*>(rec + 16 * D);
-          const uint32_t ka = pairs[g], kb = pairs[g + 8];
+        }
 #pragma unroll
-          for (int w = 0; w < D / 32; ++w)
+        for (int w = 0; w < D / 32; ++w)
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {  // codes 0, 1, 4, 5 of a word, then 2, 3, 6, 7
-              // As fp16, 0x000n is the subnormal n·2⁻²⁴ and 0x00n0 is 16n·2⁻²⁴: a code
-              // in the low byte of a half is a number already (the tensor cores take
-              // subnormals exactly).
-              const uint32_t x = w0[w] >> (8 * b), y = w1[w] >> (8 * b);
+          for (int b = 0; b < 2; ++b) {  // codes 0, 1, 4, 5 of a word, then 2, 3, 6, 7
+            uint32_t bq[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (kSharedQ) {
+                const uint2 x = s_q[2 * w + b][lane];
+                bq[nt][0] = x.x;
+                bq[nt][1] = x.y;
+              } else {
+                bq[nt][0] = qf[2 * w + b][nt][0];
+                bq[nt][1] = qf[2 * w + b][nt][1];
+              }
+            }
+            // As fp16, 0x000n is the subnormal n·2⁻²⁴ and 0x00n0 is 16n·2⁻²⁴: a code
+            // in the low byte of a half is a number already (the tensor cores take
+            // subnormals exactly).
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const uint32_t x = w0[u][w] >> (8 * b), y = w1[u][w] >> (8 * b);
               const uint32_t af[4] = {x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                if (w + b == 0) mma_first<true>(z[u][nt], af, qf[0][nt]);
-                else mma<true>(z[u][nt], af, qf[2 * w + b][nt], z[u][nt]);
+                // from −8·Σ q: the sum is of n − 8, which keeps it small
+                if (w + b == 0) mma<true>(z[u][nt], af, bq[nt], qc[nt][0], qc[nt][1], qc[nt][0], qc[nt][1]);
+                else mma<true>(z[u][nt], af, bq[nt], z[u][nt]);
               }
             }
-          const float ks0 = bf16_lo(ka), ks1 = bf16_lo(kb), kz0 = bf16_hi(ka), kz1 = bf16_hi(kb);
+          }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t* pairs = reinterpret_cast<const uint32_t*>(buf + u * (Sh::slot_bytes / U) + 16 * D);
+          const uint32_t ka = pairs[g], kb = pairs[g + 8];
+          const float ks0 = bf16_lo(ka), ks1 = bf16_lo(kb);
+          const float kz0 = fmaf(8.f, ks0, bf16_hi(ka)), kz1 = fmaf(8.f, ks1, bf16_hi(kb));  // the value of code 8
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -630,23 +701,29 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
             for (int e = 0; e < 4; ++e) z[u][nt][e] = a.cap2 * tanh_f32(z[u][nt][e]);
       }
       if (a.slopes) {
+        if (flags & 2) {  // behind the query the bias is linear
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int first = j0[u] & -kTile;
-              if (flags & 2) {  // behind the query the bias is linear
-                const float at = static_cast<float>(qd[nt][e] - first);
+              for (int e = 0; e < 2; ++e) {
+                const float at = static_cast<float>(qd[nt][e] - (j0[u] & -kTile));
                 z[u][nt][e] = fmaf(-slope2[nt][e], at, z[u][nt][e]);
                 z[u][nt][2 + e] = fmaf(-slope2[nt][e], at - 8.f, z[u][nt][2 + e]);
-              } else {
-                const int i = row_position(nt, e), d0 = i - g - qd[nt][e], off = i - first - g;
+              }
+        } else {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int i = row_position(nt, e), d0 = i - g - qd[nt][e], off = i - (j0[u] & -kTile) - g;
                 z[u][nt][e] = fmaf(-slope2[nt][e], static_cast<float>(abs(off) - d0), z[u][nt][e]);
                 z[u][nt][2 + e] = fmaf(-slope2[nt][e], static_cast<float>(abs(off - 8) - d0), z[u][nt][2 + e]);
               }
-            }
+        }
       }
       // masks: only steps that not every row sees whole
       uint32_t apart = 0;  // bf16: tokens that some rows see and others do not, with a V that is not finite
@@ -696,66 +773,145 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           __syncwarp();
         }
       }
-      // a score far above the reference: new maxima, and the state follows
-      bool grow = false;
+      // A score far above the reference: new maxima, and the state follows.
+      auto move_reference = [&](int nt, int e, float to) {
+        if (to > m[nt][e]) {
+          const float f = ex2(m[nt][e] - to);
+          m[nt][e] = to;
+          l[nt][e] *= f;
+          corr[nt][e] *= f;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+          for (int j = 0; j < MT; ++j) {
+            o[j][nt][e] *= f;
+            o[j][nt][2 + e] *= f;
+          }
+        }
+      };
+      auto max_over_tokens = [&](float x) {
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+      };
+      float w[U][NT][4];  // the weights of V: p, and for 4 bits p·step
+      float vs[U][2], vmid[U][2];  // 4 bits: V's step and the value of code 8, of tokens g and g + 8
+      if constexpr (!Q4) {
+        bool grow = false;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int u = 0; u < U; ++u) grow |= z[u][nt][e] > m[nt][e & 1] + kGrow;
-      if (__any_sync(0xffffffffu, grow)) {
+          for (int e = 0; e < 4; ++e) grow |= z[0][nt][e] > m[nt][e & 1] + kGrow;
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) move_reference(nt, e, max_over_tokens(fmaxf(z[0][nt][e], z[0][nt][2 + e])));
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[0][nt][e] = ex2(z[0][nt][e] - m[nt][e & 1]);
+            l[nt][e & 1] += w[0][nt][e];
+          }
+      } else {
+        // w = p·step·2^64, since the codes of V enter as bf16 subnormals n·2⁻¹³³.  The
+        // reference follows p·step as well as p, so that w stays in its range
+        // whatever the steps: it is the largest score plus log2(step), or the
+        // largest score less 32 where steps are below 2^-32.
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const uint32_t* pairs = reinterpret_cast<const uint32_t*>(buf + u * (Sh::slot_bytes / U) + 16 * D);
+          const uint32_t va = pairs[16 + g], vb = pairs[24 + g];
+          vs[u][0] = bf16_lo(va);
+          vs[u][1] = bf16_lo(vb);
+          vmid[u][0] = fmaf(8.f, vs[u][0], bf16_hi(va));
+          vmid[u][1] = fmaf(8.f, vs[u][1], bf16_hi(vb));
+        }
+        if (!whole) {
+          // A masked token's pair may hold anything, and 0·NaN must not reach the
+          // sums: it counts as 0 where none of the lane's rows sees the token; a row
+          // that does see one that is not finite gets its NaN through the score.
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              bool seen = false;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) seen |= z[u][nt][2 * t + e] != -INFINITY;
+              if (!seen || !(fabsf(vs[u][t]) < 0x1p63f && fabsf(vmid[u][t]) < INFINITY)) {
+                vs[u][t] = vmid[u][t] = 0.f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    if (z[u][nt][2 * t + e] != -INFINITY) z[u][nt][2 * t + e] = NAN;
+              }
+            }
+        }
+        float sum[NT][2], mid[NT][2];
+        auto weigh = [&]() {
+          bool fits = true;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              sum[nt][e] = l[nt][e];
+              mid[nt][e] = corr[nt][e];
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                  const float p = ex2(z[u][nt][2 * t + e] - m[nt][e]);
+                  sum[nt][e] += p;
+                  mid[nt][e] = fmaf(p, vmid[u][t], mid[nt][e]);
+                  w[u][nt][2 * t + e] = p * (vs[u][t] * 0x1p64f);
+                  fits = fits && w[u][nt][2 * t + e] <= 0x1p100f;
+                }
+              fits = fits && sum[nt][e] <= 0x1p100f;
+            }
+          return fits;
+        };
+        if (__any_sync(0xffffffffu, !weigh())) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = -INFINITY;
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                  const float x = z[u][nt][2 * t + e];
+                  if (x > -INFINITY) top = fmaxf(top, x + fmaxf(-32.f, __log2f(vs[u][t])));
+                }
+              move_reference(nt, e, max_over_tokens(top));
+            }
+          weigh();
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(z[0][nt][e], z[0][nt][2 + e]);
-            if constexpr (U == 2) top = fmaxf(top, fmaxf(z[U - 1][nt][e], z[U - 1][nt][2 + e]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            if (top > m[nt][e]) {
-              const float f = ex2(m[nt][e] - top);
-              m[nt][e] = top;
-              l[nt][e] *= f;
-              corr[nt][e] *= f;
-#pragma unroll
-              for (int j = 0; j < MT; ++j) {
-                o[j][nt][e] *= f;
-                o[j][nt][2 + e] *= f;
-              }
-            }
+            l[nt][e] = sum[nt][e];
+            corr[nt][e] = mid[nt][e];
           }
       }
-      // weights, and their three bf16 parts as B fragments
+      // w in three bf16 parts, as B fragments
       uint32_t pf[U][NT][3][2];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float vs[2], vmid[2];  // 4 bits: V's step and the value of code 8, of tokens g and g + 8
-        if constexpr (Q4) {
-          const uint32_t* pairs = reinterpret_cast<const uint32_t*>(buf + u * (Sh::slot_bytes / U) + 16 * D);
-          const uint32_t va = pairs[16 + g], vb = pairs[24 + g];
-          vs[0] = bf16_lo(va);
-          vs[1] = bf16_lo(vb);
-          vmid[0] = fmaf(8.f, vs[0], bf16_hi(va));
-          vmid[1] = fmaf(8.f, vs[1], bf16_hi(vb));
-        }
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[e] = ex2(z[u][nt][e] - m[nt][e & 1]);
-            l[nt][e & 1] += p[e];
-          }
           if constexpr (!Q4) {
             if (apart) {
               // tokens set apart, by hand: only rows that see them, p > 0
               const unsigned char* vt = buf + D / 64 * kTile * 128;
               for (uint32_t rest = apart; rest; rest &= rest - 1) {
                 const int tok = __ffs(rest) - 1, from = (tok & 7) * 4 + t4;
-                const float pa = __shfl_sync(0xffffffffu, tok < 8 ? p[0] : p[2], from);
-                const float pb = __shfl_sync(0xffffffffu, tok < 8 ? p[1] : p[3], from);
+                const float pa = __shfl_sync(0xffffffffu, tok < 8 ? w[0][nt][0] : w[0][nt][2], from);
+                const float pb = __shfl_sync(0xffffffffu, tok < 8 ? w[0][nt][1] : w[0][nt][3], from);
 #pragma unroll
                 for (int j = 0; j < MT; ++j)
 #pragma unroll
@@ -768,33 +924,21 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
                   }
               }
             }
-          } else if (whole) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              corr[nt][e & 1] = fmaf(p[e], vmid[e >> 1], corr[nt][e & 1]);
-              p[e] *= vs[e >> 1];
-            }
-          } else {  // a masked token's pair may hold anything
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (p[e] > 0.f) corr[nt][e & 1] = fmaf(p[e], vmid[e >> 1], corr[nt][e & 1]);
-              p[e] = p[e] > 0.f ? p[e] * vs[e >> 1] : 0.f;
-            }
           }
+          float(&x)[4] = w[u][nt];
 #pragma unroll
           for (int part = 0; part < 3; ++part) {
-            pf[u][nt][part][0] = transpose8x8(__byte_perm(__float_as_uint(p[0]), __float_as_uint(p[1]), 0x7632));
-            pf[u][nt][part][1] = transpose8x8(__byte_perm(__float_as_uint(p[2]), __float_as_uint(p[3]), 0x7632));
+            pf[u][nt][part][0] = transpose8x8(__byte_perm(__float_as_uint(x[0]), __float_as_uint(x[1]), 0x7632));
+            pf[u][nt][part][1] = transpose8x8(__byte_perm(__float_as_uint(x[2]), __float_as_uint(x[3]), 0x7632));
             if (part < 2) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                p[e] -= __uint_as_float(__float_as_uint(p[e]) & 0xffff0000u);
-                if (Q4 && part == 0) corr[nt][e & 1] = fmaf(-24.f, p[e], corr[nt][e & 1]);
+                x[e] -= __uint_as_float(__float_as_uint(x[e]) & 0xffff0000u);
+                if (Q4 && part == 0) corr[nt][e & 1] = fmaf(-0x1p-61f, x[e], corr[nt][e & 1]);
               }
             }
           }
         }
-      }
       if constexpr (!Q4) {
         if (apart) {
           stream_sync();  // the warps that share the tile have all read the rows
@@ -841,16 +985,21 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
               for (int e = 0; e < 4; ++e) o[j0v + jj][nt][e] += t[jj][nt][e];
         }
       } else {
-        // The codes enter as 16 + n (no subtraction): products with the first
-        // part of p start from −24·Σ hi, computed by the same tensor cores from a
-        // tile of −24, and give Σ hi·(n − 8) without loss, since hi has 8 bits;
-        // the other parts leave 24·Σ (mid + lo), small, which corr takes back.
-        float c24[NT][4];
-        const uint32_t m24[4] = {0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u, 0xc1c0c1c0u};
+        // As bf16, 0x000n is the subnormal n·2⁻¹³³ and 0x00n0 is 16n·2⁻¹³³ (exponent
+        // field 1 has the subnormals' spacing), so codes are numbers already.  To
+        // center them at 8, products with the first part of w start from −8·Σ hi,
+        // computed by the same tensor cores from a tile of −8·2⁻¹³³, which loses
+        // nothing, since hi has 8 bits; the other parts leave 8·Σ (mid + lo), small,
+        // which corr takes back.  Codes in the upper places come 16 times too large;
+        // their rows of the result are divided by 16 at the end.
+        float c8[NT][4], c128[NT][4];
+        const uint32_t m8[4] = {0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma_first<false>(c24[nt], m24, pf[0][nt][0]);
-          if constexpr (U == 2) mma<false>(c24[nt], m24, pf[U - 1][nt][0], c24[nt]);
+          mma_first<false>(c8[nt], m8, pf[0][nt][0]);
+          if constexpr (U == 2) mma<false>(c8[nt], m8, pf[U - 1][nt][0], c8[nt]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c128[nt][e] = 16.f * c8[nt][e];
         }
         // lane (g, t4): tokens 2·t4, 2·t4 + 1 (+ 8), numbers D/8·g … of each;
         // the byte interleave pairs the two tokens' codes of one number
@@ -890,10 +1039,11 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
             for (int jj = 0; jj < JB; ++jj) {
               // m rows g: number j of the lane's share; rows g + 8: number MT + j
               const int j = j0v + jj;
-              af[u][jj][0] = q4_pair16(un[u][0][j / 4], j & 3);
-              af[u][jj][1] = q4_pair16(un[u][0][MT / 4 + j / 4], j & 3);
-              af[u][jj][2] = q4_pair16(un[u][1][j / 4], j & 3);
-              af[u][jj][3] = q4_pair16(un[u][1][MT / 4 + j / 4], j & 3);
+              const uint32_t mask = j & 1 ? 0x00f000f0u : 0x000f000fu;
+              af[u][jj][0] = (un[u][0][j / 4] >> (8 * (j >> 1 & 1))) & mask;
+              af[u][jj][1] = (un[u][0][MT / 4 + j / 4] >> (8 * (j >> 1 & 1))) & mask;
+              af[u][jj][2] = (un[u][1][j / 4] >> (8 * (j >> 1 & 1))) & mask;
+              af[u][jj][3] = (un[u][1][MT / 4 + j / 4] >> (8 * (j >> 1 & 1))) & mask;
             }
 #pragma unroll
           for (int part = 0; part < 3; ++part)
@@ -903,7 +1053,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
               for (int jj = 0; jj < JB; ++jj)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  if (part == 0 && u == 0) mma<false>(t[jj][nt], af[u][jj], pf[u][nt][part], c24[nt]);
+                  if (part == 0 && u == 0) mma<false>(t[jj][nt], af[u][jj], pf[u][nt][part], (j0v + jj) & 1 ? c128[nt] : c8[nt]);
                   else mma<false>(t[jj][nt], af[u][jj], pf[u][nt][part], t[jj][nt]);
                 }
 #pragma unroll
@@ -971,8 +1121,10 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
         float* to = red + (warp * 8 * NT + row) * PITCH;
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
-          to[Q4 ? D / 8 * g + j : 16 * j + g] = o[j][nt][e] * f;
-          to[Q4 ? D / 8 * g + MT + j : 16 * j + 8 + g] = o[j][nt][2 + e] * f;
+          // 4 bits: back from 2^(64 − 133), and from 16 times that for odd j
+          const float by = Q4 ? f * (j & 1 ? 0x1p65f : 0x1p69f) : f;
+          to[merge_at<D, Q4>(Q4 ? D / 8 * g + j : 16 * j + g)] = o[j][nt][e] * by;
+          to[merge_at<D, Q4>(Q4 ? D / 8 * g + MT + j : 16 * j + 8 + g)] = o[j][nt][2 + e] * by;
         }
       }
     __syncthreads();
@@ -988,7 +1140,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         const int w = s * R + r;
-        const float4 x = *reinterpret_cast<const float4*>(red + (w * 8 * NT + in) * PITCH + c);
+        const float* from = red + (w * 8 * NT + in) * PITCH + merge_at<D, Q4>(c);
+        const float4 x = Q4 ? make_float4(from[0], from[1], from[2], from[3]) : *reinterpret_cast<const float4*>(from);
         const float f = s_m[w][in] > -INFINITY ? ex2(s_m[w][in] - top) : 0.f;
         sum.x += x.x;
         sum.y += x.y;
@@ -1173,7 +1326,7 @@ cudaError_t launch_softmax_mod(const ekv_cache& c, const void* pool, const ekv_s
   a.num_phys = c.num_phys_pages;
   a.max_pages = s.max_pages;
   a.cap = cap;
-  a.min_tiles = 8;
+  a.min_tiles = pool ? 8 : 4;
   a.slack_tiles = pool ? 32 : 12;
   a.scale2 = scale * kLog2e;
   if (mod != nullptr) {
