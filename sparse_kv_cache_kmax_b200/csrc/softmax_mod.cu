@@ -24,7 +24,6 @@
 //
 // The bound is HBM: 512 bytes per bf16 (token, KV head), 136 in 4 bits.
 #include <cuda.h>
-#include <cuda_fp16.h>
 
 #include "q4.cuh"
 
@@ -79,31 +78,21 @@ __device__ __forceinline__ float tanh_f32(float x) {
   return x != x ? x : copysignf(t, x);
 }
 
-// d = A·B + c on m16n8k16 (fragments as mma_bf16 in common.cuh), bf16 or fp16
-// operands.  d and c apart, and no volatile: the compiler is free to interleave
-// the products of several rows.
-template <bool Half>
+// d = A·B + c on m16n8k16 bf16 (fragments as mma_bf16 in common.cuh).  d and c
+// apart, and no volatile: the compiler is free to interleave products.
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2], float c0, float c1,
                                     float c2, float c3) {
-  if constexpr (Half)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %11, %12, %13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%10, %11, %12, %13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
-template <bool Half>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2],
                                     const float (&c)[4]) {
-  mma<Half>(d, a, b, c[0], c[1], c[2], c[3]);
+  mma(d, a, b, c[0], c[1], c[2], c[3]);
 }
-template <bool Half>
 __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  mma<Half>(d, a, b, 0.f, 0.f, 0.f, 0.f);
+  mma(d, a, b, 0.f, 0.f, 0.f, 0.f);
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -527,11 +516,10 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           qf[ks][nt][1] = q_raw[nt][2 * ks + 1];
         }
       } else {
-        // fp16, scaled by a power of two to a largest number in [2^14, 2^15): bf16's
-        // 8 bits fit, and what falls below fp16's range is under 2^-38 of the
-        // largest.  Word w of the lane's share gives the pairs (8w + i, 8w + i + 4),
-        // as the codes do; codes at odd i come 16 times too large, so their
-        // numbers are divided by 16.
+        // Scaled by a power of two to a largest number near 2^100 (exact: the codes
+        // enter as subnormals n·2⁻¹³³).  Word w of the lane's share gives the pairs
+        // (8w + i, 8w + i + 4), as the codes do; codes at odd i come 16 times too
+        // large, so their numbers are divided by 16.
         float sum = 0.f, top = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
@@ -543,7 +531,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int k = 14 + 127 - static_cast<int>(__float_as_uint(top) >> 23);
+        const int k = 100 + 127 - static_cast<int>(__float_as_uint(top) >> 23);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + max(-126, min(126, k))) << 23);
         uint32_t qh[KS][2];
 #pragma unroll
@@ -552,9 +540,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           for (int i = 0; i < 4; ++i) {
             const float by = (i & 1) ? up * 0.0625f : up;
             const uint32_t x = q_raw[nt][4 * w + (i >> 1)], y = q_raw[nt][4 * w + 2 + (i >> 1)];
-            const __half2 h = (i & 1) ? __floats2half2_rn(bf16_hi(x) * by, bf16_hi(y) * by)
-                                      : __floats2half2_rn(bf16_lo(x) * by, bf16_lo(y) * by);
-            qh[2 * w + (i >> 1)][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
+            qh[2 * w + (i >> 1)][i & 1] = (i & 1) ? pack_bf16_exact(bf16_hi(x) * by, bf16_hi(y) * by)
+                                                  : pack_bf16_exact(bf16_lo(x) * by, bf16_lo(y) * by);
           }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -565,10 +552,10 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
             qf[ks][nt][1] = qh[ks][1];
           }
         }
-        const float zf = a.cap2 != 0.f ? a.capx : a.scale2, down = zf / up * 16777216.f;
+        const float zf = a.cap2 != 0.f ? a.capx : a.scale2, down = zf * 0x1p66f / up * 0x1p67f;
         qsum[nt][0] = __shfl_sync(0xffffffffu, sum * zf, 8 * t4);
         qsum[nt][1] = __shfl_sync(0xffffffffu, sum * zf, 8 * t4 + 4);
-        const float c8 = sum * up * -0x1p-21f;
+        const float c8 = sum * up * -0x1p-65f * 0x1p-65f;
         qc[nt][0] = __shfl_sync(0xffffffffu, c8, 8 * t4);
         qc[nt][1] = __shfl_sync(0xffffffffu, c8, 8 * t4 + 4);
         qdown[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t4);
@@ -622,8 +609,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float(&to)[4] = ks & 1 ? z2[nt] : z[0][nt];
-            if (ks < 2) mma_first<false>(to, af, qf[ks][nt]);
-            else mma<false>(to, af, qf[ks][nt], to);
+            if (ks < 2) mma_first(to, af, qf[ks][nt]);
+            else mma(to, af, qf[ks][nt], to);
           }
         }
         const float zf = a.cap2 != 0.f ? a.capx : a.scale2;
@@ -662,9 +649,10 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
                 bq[nt][1] = qf[2 * w + b][nt][1];
               }
             }
-            // As fp16, 0x000n is the subnormal n·2⁻²⁴ and 0x00n0 is 16n·2⁻²⁴: a code
-            // in the low byte of a half is a number already (the tensor cores take
-            // subnormals exactly).
+            // As bf16, 0x000n is the subnormal n·2⁻¹³³ and 0x00n0 is 16n·2⁻¹³³ (exponent
+            // field 1 has the subnormals' spacing): a code in the low byte of a half
+            // is a number already.  (fp16 would do too, but the tensor cores align sums
+            // by exponent fields: there the products lost three bits more.)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               const uint32_t x = w0[u][w] >> (8 * b), y = w1[u][w] >> (8 * b);
@@ -672,8 +660,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 // from −8·Σ q: the sum is of n − 8, which keeps it small
-                if (w + b == 0) mma<true>(z[u][nt], af, bq[nt], qc[nt][0], qc[nt][1], qc[nt][0], qc[nt][1]);
-                else mma<true>(z[u][nt], af, bq[nt], z[u][nt]);
+                if (w + b == 0) mma(z[u][nt], af, bq[nt], qc[nt][0], qc[nt][1], qc[nt][0], qc[nt][1]);
+                else mma(z[u][nt], af, bq[nt], z[u][nt]);
               }
             }
           }
@@ -974,8 +962,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
             for (int jj = 0; jj < JB; ++jj)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                if (part == 2) mma_first<false>(t[jj][nt], af[jj], pf[0][nt][part]);
-                else mma<false>(t[jj][nt], af[jj], pf[0][nt][part], t[jj][nt]);
+                if (part == 2) mma_first(t[jj][nt], af[jj], pf[0][nt][part]);
+                else mma(t[jj][nt], af[jj], pf[0][nt][part], t[jj][nt]);
               }
 #pragma unroll
           for (int jj = 0; jj < JB; ++jj)
@@ -985,22 +973,22 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
               for (int e = 0; e < 4; ++e) o[j0v + jj][nt][e] += t[jj][nt][e];
         }
       } else {
-        // As bf16, 0x000n is the subnormal n·2⁻¹³³ and 0x00n0 is 16n·2⁻¹³³ (exponent
-        // field 1 has the subnormals' spacing), so codes are numbers already.  To
-        // center them at 8, products with the first part of w start from −8·Σ hi,
+        // The codes are numbers already, as K's.  To center them at 8, products with the first part of w start from −8·Σ hi,
         // computed by the same tensor cores from a tile of −8·2⁻¹³³, which loses
         // nothing, since hi has 8 bits; the other parts leave 8·Σ (mid + lo), small,
         // which corr takes back.  Codes in the upper places come 16 times too large;
         // their rows of the result are divided by 16 at the end.
-        float c8[NT][4], c128[NT][4];
+        float c8[U][NT][2];
         const uint32_t m8[4] = {0x80088008u, 0x80088008u, 0x80088008u, 0x80088008u};
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_first<false>(c8[nt], m8, pf[0][nt][0]);
-          if constexpr (U == 2) mma<false>(c8[nt], m8, pf[U - 1][nt][0], c8[nt]);
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) c128[nt][e] = 16.f * c8[nt][e];
-        }
+          for (int nt = 0; nt < NT; ++nt) {
+            float t[4];
+            mma_first(t, m8, pf[u][nt][0]);
+            c8[u][nt][0] = t[0];
+            c8[u][nt][1] = t[1];
+          }
         // lane (g, t4): tokens 2·t4, 2·t4 + 1 (+ 8), numbers D/8·g … of each;
         // the byte interleave pairs the two tokens' codes of one number
         constexpr int VW = D / 64;  // words per lane and token
@@ -1032,7 +1020,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
 #pragma unroll
         for (int j0v = 0; j0v < MT; j0v += JB) {
           uint32_t af[U][JB][4];
-          float t[JB][NT][4];
+          float t[U][JB][NT][4];
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -1053,15 +1041,20 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
               for (int jj = 0; jj < JB; ++jj)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  if (part == 0 && u == 0) mma<false>(t[jj][nt], af[u][jj], pf[u][nt][part], (j0v + jj) & 1 ? c128[nt] : c8[nt]);
-                  else mma<false>(t[jj][nt], af[u][jj], pf[u][nt][part], t[jj][nt]);
+                  const float by = (j0v + jj) & 1 ? 16.f : 1.f, a0 = c8[u][nt][0] * by, a1 = c8[u][nt][1] * by;
+                  if (part == 0) mma(t[u][jj][nt], af[u][jj], pf[u][nt][part], a0, a1, a0, a1);
+                  else mma(t[u][jj][nt], af[u][jj], pf[u][nt][part], t[u][jj][nt]);
                 }
 #pragma unroll
           for (int jj = 0; jj < JB; ++jj)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[j0v + jj][nt][e] += t[jj][nt][e];
+              for (int e = 0; e < 4; ++e) {
+                float sum = t[0][jj][nt][e];
+                if constexpr (U == 2) sum += t[U - 1][jj][nt][e];
+                o[j0v + jj][nt][e] += sum;
+              }
         }
       }
       // the slot is free: the next copies into it
