@@ -38,6 +38,7 @@ struct AppendArgs {
   int64_t q_stride, k_stride, v_stride;
   int max_pos, rot, interleaved;
   int batch, rows, Hkv, G, S, num_phys, max_pages;
+  int heads;  // KV heads (or their query groups) that one CTA takes in turn
 };
 
 // The new tokens of one page: slots lo .. hi−1; slot s is row `row + s − lo`.
@@ -111,28 +112,83 @@ __device__ __forceinline__ void store8(float* p, const float* v) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// Units of work of one row of d numbers, eight or twice eight of them each:
-// half-split pairs take chunk u of the first half of rot with its partner;
-// everything else is one chunk.  A unit owns all it reads, so a row may be
-// rotated in place.
-__device__ __forceinline__ int row_units(int D, int rot, int interleaved) {
-  return interleaved ? D / 8 : (D - rot / 2) / 8;
+// A row of d numbers is rotated in units of eight numbers or, for half-split
+// pairs, of eight and their eight partners; a unit owns all it reads, so a row
+// may be rotated in place.  The threads of a CTA are laid out as a power of two
+// of units (slots) by rows, so that nothing is divided.
+struct Layout {
+  int units, slots;  // units per row, and the power of two above
+  int u, r0, step;   // this thread's unit, first row, and the rows of one pass
+};
+__device__ __forceinline__ Layout row_layout(int D, int rot, int interleaved) {
+  Layout l;
+  l.units = interleaved ? D / 8 : (D - rot / 2) / 8;
+  l.slots = l.units > 8 ? 16 : (l.units > 4 ? 8 : 4);
+  const int shift = l.units > 8 ? 4 : (l.units > 4 ? 3 : 2);
+  l.u = threadIdx.x & (l.slots - 1);
+  l.r0 = threadIdx.x >> shift;
+  l.step = kThreads >> shift;
+  return l;
+}
+// Cosines and sines of a unit (as many as it has pairs: eight, four, or none).
+struct Turn {
+  float c[8], s[8];
+};
+__device__ __forceinline__ void load_turn(Turn& t, const float* cs, int u, int rot, int interleaved) {
+  const int half = rot / 2;
+  if (!interleaved && u < half / 8) {
+    load8(cs + 8 * u, t.c);
+    load8(cs + half + 8 * u, t.s);
+  } else if (interleaved && 8 * u < rot) {
+    load4(cs + 4 * u, t.c);
+    load4(cs + half + 4 * u, t.s);
+  }
+}
+// The raw bits of a unit: its eight numbers, and its partners' where it has any.
+template <typename T>
+struct Raw {
+  uint4 x[sizeof(T) / 2], z[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void load_raw(Raw<T>& r, const T* src, int u, int rot, int interleaved) {
+  const int half = rot / 2;
+  const bool split = !interleaved && u < half / 8;
+  const T* p = src + (interleaved || split ? 8 * u : half + 8 * u);
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.x[i] = reinterpret_cast<const uint4*>(p)[i];
+  if (split) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.z[i] = reinterpret_cast<const uint4*>(p + half)[i];
+  }
 }
 template <typename T>
-__device__ __forceinline__ void rotate_unit(const T* src, T* dst, T* dst2, const float* cs, int u, int rot,
+__device__ __forceinline__ void widen8(const uint4 (&w)[sizeof(T) / 2], float* v) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t ws[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(ws[i]);
+      v[2 * i + 1] = bf16_hi(ws[i]);
+    }
+  } else {
+    const uint32_t ws[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(ws[i]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void rotate_unit(const Raw<T>& r, const Turn& t, T* dst, T* dst2, int u, int rot,
                                             int interleaved) {
   const int half = rot / 2;
   float x[8], y[8];
+  widen8<T>(r.x, x);
   if (!interleaved && u < half / 8) {
-    float z[8], c[8], s[8];
-    load8(src + 8 * u, x);
-    load8(src + half + 8 * u, z);
-    load8(cs + 8 * u, c);
-    load8(cs + half + 8 * u, s);
+    float z[8];
+    widen8<T>(r.z, z);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      y[i] = fmaf(x[i], c[i], -z[i] * s[i]);
-      z[i] = fmaf(z[i], c[i], x[i] * s[i]);
+      y[i] = fmaf(x[i], t.c[i], -z[i] * t.s[i]);
+      z[i] = fmaf(z[i], t.c[i], x[i] * t.s[i]);
     }
     store8(dst + 8 * u, y);
     store8(dst + half + 8 * u, z);
@@ -143,15 +199,11 @@ __device__ __forceinline__ void rotate_unit(const T* src, T* dst, T* dst2, const
     return;
   }
   const int j = interleaved ? 8 * u : half + 8 * u;
-  load8(src + j, x);
   if (interleaved && j < rot) {
-    float c[4], s[4];
-    load4(cs + j / 2, c);
-    load4(cs + half + j / 2, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      y[2 * i] = fmaf(x[2 * i], c[i], -x[2 * i + 1] * s[i]);
-      y[2 * i + 1] = fmaf(x[2 * i + 1], c[i], x[2 * i] * s[i]);
+      y[2 * i] = fmaf(x[2 * i], t.c[i], -x[2 * i + 1] * t.s[i]);
+      y[2 * i + 1] = fmaf(x[2 * i + 1], t.c[i], x[2 * i] * t.s[i]);
     }
   } else {
 #pragma unroll
@@ -161,38 +213,65 @@ __device__ __forceinline__ void rotate_unit(const T* src, T* dst, T* dst2, const
   if (dst2) store8(dst2 + j, y);
 }
 
-// Rotates the G query heads of KV head h for a page's new tokens.
+// Rotates the query heads of KV heads h0 .. h1−1 for a page's new tokens: a
+// thread keeps its token's angles and takes heads in turn, four rows' loads at
+// a time.
 template <typename T, int D>
-__device__ void rotate_queries(const AppendArgs& a, const PageItem& it, int h) {
-  const int units = row_units(D, a.rot, a.interleaved), per_tok = units * a.G, n = it.hi - it.lo;
-  const int Hq = a.Hkv * a.G;
-  for (int i = threadIdx.x; i < n * per_tok; i += kThreads) {
-    const int t = i / per_tok, r = i - t * per_tok, g = r / units, u = r - g * units;
-    const int row = it.row + t, head = h * a.G + g;
-    const float* cs = a.rot ? rotation_row(a, it.pos + it.lo + t) : nullptr;
-    rotate_unit<T>(static_cast<const T*>(a.q) + row * a.q_stride + static_cast<int64_t>(head) * D,
-                   static_cast<T*>(a.q_out) + (static_cast<int64_t>(row) * Hq + head) * D, nullptr, cs, u, a.rot,
-                   a.interleaved);
+__device__ void rotate_queries(const AppendArgs& a, const PageItem& it, int h0, int h1) {
+  const Layout l = row_layout(D, a.rot, a.interleaved);
+  const int n = it.hi - it.lo, Hq = a.Hkv * a.G;
+  if (l.u >= l.units) return;
+  int toks = 1;  // tokens side by side: a power of two, the rest of the rows are heads
+  while (toks < n && toks < l.step) toks <<= 1;
+  const int tsh = __ffs(toks) - 1, heads = l.step >> tsh;
+  const int first = h0 * a.G + (l.r0 >> tsh), last = h1 * a.G;
+  for (int t = l.r0 & (toks - 1); t < n; t += toks) {
+    Turn turn;
+    if (a.rot) load_turn(turn, rotation_row(a, it.pos + it.lo + t), l.u, a.rot, a.interleaved);
+    const int row = it.row + t;
+    const T* src = static_cast<const T*>(a.q) + row * a.q_stride;
+    T* dst = static_cast<T*>(a.q_out) + static_cast<int64_t>(row) * Hq * D;
+    constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
+    for (int hq = first; hq < last; hq += kAhead * heads) {
+      Raw<T> raw[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        load_raw<T>(raw[i], src + static_cast<int64_t>(min(hq + i * heads, last - 1)) * D, l.u, a.rot, a.interleaved);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (hq + i * heads < last)
+          rotate_unit<T>(raw[i], turn, dst + static_cast<int64_t>(hq + i * heads) * D, static_cast<T*>(nullptr), l.u,
+                         a.rot, a.interleaved);
+    }
   }
 }
 
 // Metadata of one coordinate over tokens 0..n−1 of a page, as meta.cu computes
 // it: exact extremes, mean and population variance in float64 in token order
-// with one rounding per operation.
-template <class F>
+// with one rounding per operation.  P: 16 or 32, at least n; value(t) is called
+// for every t < P, in one batch.
+template <int P, class F>
 __device__ __forceinline__ void column_meta(F value, int n, float* mx, float* mn, double* mean, double* var) {
+  float x[P];
+#pragma unroll
+  for (int t = 0; t < P; ++t) x[t] = value(t);
   float hi = -INFINITY, lo = INFINITY;
   double s = 0.0, v = 0.0;
-  for (int t = 0; t < n; ++t) {
-    const float x = value(t);
-    hi = fmaxf(hi, x);
-    lo = fminf(lo, x);
-    s = __dadd_rn(s, static_cast<double>(x));
+#pragma unroll
+  for (int t = 0; t < P; ++t) {
+    if (t < n) {
+      hi = fmaxf(hi, x[t]);
+      lo = fminf(lo, x[t]);
+      s = __dadd_rn(s, static_cast<double>(x[t]));
+    }
   }
   const double dn = static_cast<double>(n), m = __ddiv_rn(s, dn);
-  for (int t = 0; t < n; ++t) {
-    const double d = __dsub_rn(static_cast<double>(value(t)), m);
-    v = __dadd_rn(v, __dmul_rn(d, d));
+#pragma unroll
+  for (int t = 0; t < P; ++t) {
+    if (t < n) {
+      const double d = __dsub_rn(static_cast<double>(x[t]), m);
+      v = __dadd_rn(v, __dmul_rn(d, d));
+    }
   }
   *mx = hi;
   *mn = lo;
@@ -200,82 +279,129 @@ __device__ __forceinline__ void column_meta(F value, int n, float* mx, float* mn
   *var = __ddiv_rn(v, dn);
 }
 
-// grid: (items, Hkv for K and V, then Hkv more for the queries).
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(AppendArgs a) {
+// grid: (items, CTAs for K and V, then as many for the queries); a CTA takes
+// a.heads KV heads in turn: the lookup of its page costs four dependent loads,
+// which one head of a prompt's page does not pay for.
+template <typename T, int D, int S>
+__global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(AppendArgs a) {
   grid_dep_enter();
   PageItem it;
   if (!page_item(a, blockIdx.x, &it)) return;
-  if (static_cast<int>(blockIdx.y) >= a.Hkv) {
-    rotate_queries<T, D>(a, it, blockIdx.y - a.Hkv);
+  const int per = (a.Hkv + a.heads - 1) / a.heads;  // CTAs for K and V
+  const int y = static_cast<int>(blockIdx.y), h0 = (y < per ? y : y - per) * a.heads, h1 = min(a.Hkv, h0 + a.heads);
+  if (y >= per) {
+    rotate_queries<T, D>(a, it, h0, h1);
     return;
   }
-  __shared__ __align__(16) T tile[32 * D];
-  const int h = blockIdx.y, n = it.hi - it.lo;
-  const size_t ph = static_cast<size_t>(it.phys) * a.Hkv + h;
-  T* kp = static_cast<T*>(a.k_pool) + ph * a.S * D;
-  T* vp = static_cast<T*>(a.v_pool) + ph * a.S * D;
-  constexpr int kChunk = 16 / sizeof(T), kChunks = D / kChunk;
-  const T* vsrc = static_cast<const T*>(a.v) + static_cast<int64_t>(h) * D;
-  for (int i = threadIdx.x; i < n * kChunks; i += kThreads) {
-    const int t = i / kChunks, c = (i - t * kChunks) * kChunk;
-    *reinterpret_cast<uint4*>(vp + (it.lo + t) * D + c) =
-        *reinterpret_cast<const uint4*>(vsrc + (it.row + t) * a.v_stride + c);
+  __shared__ __align__(16) T tile[S * D];
+  const int n = it.hi - it.lo;
+  constexpr int kChunk = 16 / sizeof(T), kChunks = D / kChunk, kRows = kThreads / kChunks, kPasses = S / kRows;
+  const Layout l = row_layout(D, a.rot, a.interleaved);
+  const int vrow = threadIdx.x / kChunks, vcol = (threadIdx.x % kChunks) * kChunk;
+  for (int h = h0; h < h1; ++h) {
+    const size_t ph = static_cast<size_t>(it.phys) * a.Hkv + h;
+    T* kp = static_cast<T*>(a.k_pool) + ph * S * D;
+    T* vp = static_cast<T*>(a.v_pool) + ph * S * D;
+    const T* vsrc = static_cast<const T*>(a.v) + static_cast<int64_t>(h) * D + vcol;
+    const T* ksrc = static_cast<const T*>(a.k) + static_cast<int64_t>(h) * D;
+    uint4 v[kPasses];  // all of V's loads, then K's, then the work
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int t = min(vrow + i * kRows, n - 1);
+      v[i] = *reinterpret_cast<const uint4*>(vsrc + (it.row + t) * a.v_stride);
+    }
+    if (l.u < l.units) {
+      for (int t = l.r0; t < n; t += l.step) {
+        const int slot = it.lo + t;
+        Raw<T> raw;
+        Turn turn;
+        load_raw<T>(raw, ksrc + (it.row + t) * a.k_stride, l.u, a.rot, a.interleaved);
+        if (a.rot) load_turn(turn, rotation_row(a, it.pos + slot), l.u, a.rot, a.interleaved);
+        rotate_unit<T>(raw, turn, kp + slot * D, tile + slot * D, l.u, a.rot, a.interleaved);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int t = vrow + i * kRows;
+      if (t < n) *reinterpret_cast<uint4*>(vp + (it.lo + t) * D + vcol) = v[i];
+    }
+    if (a.box == nullptr) continue;
+    for (int i = threadIdx.x; i < it.lo * kChunks; i += kThreads)
+      *reinterpret_cast<uint4*>(tile + i * kChunk) = *reinterpret_cast<const uint4*>(kp + i * kChunk);
+    __syncthreads();
+    const int j = threadIdx.x;
+    if (j < D) {
+      float mx, mn;
+      double mean, var;
+      column_meta<S>([&](int t) { return to_f32(tile[t * D + j]); }, it.hi, &mx, &mn, &mean, &var);
+      const size_t mh = (static_cast<size_t>(h) * a.num_phys + it.phys) * 2 * D + j;
+      T* box = static_cast<T*>(a.box);
+      T* mom = static_cast<T*>(a.mom);
+      box[mh] = round_store<T>(mx);
+      box[mh + D] = round_store<T>(mn);
+      mom[mh] = round_store<T>(mean);
+      mom[mh + D] = round_store<T>(var);
+    }
+    if (h + 1 < h1) __syncthreads();  // the tile is read before the next head's keys enter it
   }
-  const int units = row_units(D, a.rot, a.interleaved);
-  const T* ksrc = static_cast<const T*>(a.k) + static_cast<int64_t>(h) * D;
-  for (int i = threadIdx.x; i < n * units; i += kThreads) {
-    const int t = i / units, u = i - t * units, slot = it.lo + t;
-    const float* cs = a.rot ? rotation_row(a, it.pos + slot) : nullptr;
-    rotate_unit<T>(ksrc + (it.row + t) * a.k_stride, kp + slot * D, tile + slot * D, cs, u, a.rot, a.interleaved);
-  }
-  if (a.box == nullptr) return;
-  for (int i = threadIdx.x; i < it.lo * kChunks; i += kThreads)
-    *reinterpret_cast<uint4*>(tile + i * kChunk) = *reinterpret_cast<const uint4*>(kp + i * kChunk);
-  __syncthreads();
-  const int j = threadIdx.x;
-  if (j >= D) return;
-  float mx, mn;
-  double mean, var;
-  column_meta([&](int t) { return to_f32(tile[t * D + j]); }, it.hi, &mx, &mn, &mean, &var);
-  const size_t mh = (static_cast<size_t>(h) * a.num_phys + it.phys) * 2 * D + j;
-  T* box = static_cast<T*>(a.box);
-  T* mom = static_cast<T*>(a.mom);
-  box[mh] = round_store<T>(mx);
-  box[mh + D] = round_store<T>(mn);
-  mom[mh] = round_store<T>(mean);
-  mom[mh + D] = round_store<T>(var);
 }
 
-// One row of D numbers, D/32 of them per lane (in 64 bits), to codes: the
-// lane's codes come back packed, the pair (step, zero) on every lane.  The
-// quotient runs in fp32, off by at most 3·2⁻²⁴·15.5 < 3e-6; within 2e-5 of a
-// border between two codes it is divided again in 64 bits.
-template <int E>
-__device__ __forceinline__ uint32_t quantise_row(const double (&y)[E], uint32_t* step_zero) {
-  double mn = y[0], mx = y[0];
+// Whether x, off by at most e, may round to two different bf16 numbers.
+__device__ __forceinline__ bool near_bf16_border(float x, float e) {
+  const uint32_t b = __float_as_uint(x);
+  const float ulp = __uint_as_float(max(b & 0x7f800000u, 24u << 23) - (23u << 23));
+  return fabsf(static_cast<float>(static_cast<int>(b & 0xffffu) - 0x8000)) * ulp <= e;
+}
+
+// One row of D numbers, D/32 of them per lane, to codes: the lane's codes come
+// back packed, the pair (step, zero) on every lane.  x: the numbers in fp32,
+// each off by at most err (one bound for the row); exact(e) gives number e in
+// 64 bits.  Nearly every row is decided in fp32: only where the extremes are
+// near a border between two bf16 numbers, or a quotient near one between two
+// codes, are the exact numbers asked (1 row and 1 number in some ten thousand).
+// All in 64 bits cost 1500 issue slots per token and KV head, 4 times as many.
+template <int E, class F>
+__device__ __forceinline__ uint32_t quantise_row(const float (&x)[E], float err, F exact, uint32_t* step_zero) {
+  float mn = x[0], mx = x[0];
 #pragma unroll
   for (int e = 1; e < E; ++e) {
-    mn = fmin(mn, y[e]);
-    mx = fmax(mx, y[e]);
+    mn = fminf(mn, x[e]);
+    mx = fmaxf(mx, x[e]);
   }
+  asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(mn) : "f"(mn));
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mx) : "f"(mx));
+  float step = (mx - mn) * (1.0f / 15.0f), zero = mn;
+  // step: 2·err of the extremes, and three roundings of fp32
+  if (near_bf16_border(step, err * 0.14f + fabsf(step) * 0x1p-22f) || (err > 0.f && near_bf16_border(mn, err)) ||
+      !(mx - mn <= 3e38f)) {
+    double dmn = exact(0), dmx = dmn;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mn = fmin(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int e = 1; e < E; ++e) {
+      dmn = fmin(dmn, exact(e));
+      dmx = fmax(dmx, exact(e));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      dmn = fmin(dmn, __shfl_xor_sync(0xffffffffu, dmn, o));
+      dmx = fmax(dmx, __shfl_xor_sync(0xffffffffu, dmx, o));
+    }
+    step = __double2float_rn((dmx - dmn) / 15.0);
+    zero = __double2float_rn(dmn);
   }
-  bf16 sb = __float2bfloat16_rn(__double2float_rn((mx - mn) / 15.0));
+  bf16 sb = __float2bfloat16_rn(step);
   if (!(__bfloat162float(sb) >= 1e-30f)) sb = __ushort_as_bfloat16(0);
-  const bf16 zb = __float2bfloat16_rn(__double2float_rn(mn));
-  const float step = __bfloat162float(sb), inv = step > 0.f ? 1.0f / step : 0.f;
-  const double zero = __bfloat162float(zb);
+  const bf16 zb = __float2bfloat16_rn(zero);
+  step = __bfloat162float(sb);
+  zero = __bfloat162float(zb);
+  const float inv = step > 0.f ? 1.0f / step : 0.f;
   uint32_t codes = 0;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const double d = y[e] - zero;
-    const float f = __double2float_rn(d) * inv;
+    const float f = (x[e] - zero) * inv;
     float n = rintf(f);
-    if (fabsf(f - n) > 0.5f - 2e-5f && step > 0.f) n = __double2float_rn(rint(d / static_cast<double>(step)));
+    // f is off by err·inv, three roundings of at most 16·2⁻²⁴, and the rounding of x − zero
+    if (fabsf(f - n) > 0.5f - 4e-6f - err * inv && step > 0.f)
+      n = __double2float_rn(rint((exact(e) - static_cast<double>(zero)) / static_cast<double>(step)));
     codes |= static_cast<uint32_t>(fminf(fmaxf(n, 0.f), 15.f)) << (4 * e);
   }
   *step_zero = static_cast<uint32_t>(__bfloat16_as_ushort(sb)) |
@@ -298,103 +424,130 @@ __device__ __forceinline__ void load_lane(const T* p, float (&v)[E]) {
   }
 }
 
-// grid as rope_append_kernel; a warp takes one row (K or V of one token) at a
-// time, D/32 numbers per lane.  The products of the rotation are exact in 64
-// bits (24 + 24 bits), so its sums are rounded once, at 2⁻⁵³.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) rope_append_q4_kernel(AppendArgs a) {
+// grid as rope_append_kernel; a warp takes one token's K and V at a time, D/32
+// numbers of each per lane.  A key's exact rotated numbers, where they are
+// asked for: the products are exact in 64 bits (24 + 24 bits), so their sum is
+// rounded once, at 2⁻⁵³.
+template <typename T, int D, int S>
+__global__ void __launch_bounds__(kThreads, 5) rope_append_q4_kernel(AppendArgs a) {
   grid_dep_enter();
   PageItem it;
   if (!page_item(a, blockIdx.x, &it)) return;
-  if (static_cast<int>(blockIdx.y) >= a.Hkv) {
-    rotate_queries<T, D>(a, it, blockIdx.y - a.Hkv);
+  const int per = (a.Hkv + a.heads - 1) / a.heads;  // CTAs for K and V
+  const int by = static_cast<int>(blockIdx.y), h0 = (by < per ? by : by - per) * a.heads, h1 = min(a.Hkv, h0 + a.heads);
+  if (by >= per) {
+    rotate_queries<T, D>(a, it, h0, h1);
     return;
   }
-  constexpr int E = D / 32, R = q4_record_bytes(D), kRow = D / 2;
-  __shared__ __align__(16) unsigned char codes_s[32 * kRow];
-  __shared__ uint32_t sz_s[32];
-  const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = it.hi - it.lo;
-  unsigned char* page = static_cast<unsigned char*>(a.k_pool) +
-                        (static_cast<size_t>(it.phys) * a.Hkv + h) * (a.S / kTile) * R;
+  constexpr int E = D / 32, R = q4_record_bytes(D), kRow = D / 2, kWarps = kThreads / 32;
+  __shared__ __align__(16) unsigned char codes_s[S * kRow];
+  __shared__ uint32_t sz_s[S];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = it.hi - it.lo;
   const int j = lane * E, half = a.rot / 2;
-  for (int i = warp; i < 2 * n; i += kThreads / 32) {
-    const int t = i >> 1, isv = i & 1, slot = it.lo + t;
-    double y[E];
-    float x[E];
-    if (isv) {
-      load_lane<T, E>(static_cast<const T*>(a.v) + (it.row + t) * a.v_stride + h * D + j, x);
+  // this lane's partners and angles: number j + e pairs with j + e + half, − half, or its neighbour
+  const bool turns = j < a.rot, low = a.interleaved || j < half;
+  const int other = !turns || a.interleaved ? j : (low ? j + half : j - half);
+  const int angle = a.interleaved ? j / 2 : (low ? j : j - half);
+  for (int h = h0; h < h1; ++h) {
+    unsigned char* page = static_cast<unsigned char*>(a.k_pool) +
+                          (static_cast<size_t>(it.phys) * a.Hkv + h) * (S / kTile) * R;
+    const T* ksrc = static_cast<const T*>(a.k) + static_cast<int64_t>(h) * D;
+    const T* vsrc = static_cast<const T*>(a.v) + static_cast<int64_t>(h) * D;
+    for (int t = warp; t < n; t += kWarps) {
+      const int slot = it.lo + t;
+      float x[E], z[E], v[E], c[E], s[E];
+      load_lane<T, E>(ksrc + (it.row + t) * a.k_stride + j, x);
+      load_lane<T, E>(ksrc + (it.row + t) * a.k_stride + other, z);
+      load_lane<T, E>(vsrc + (it.row + t) * a.v_stride + j, v);
 #pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = x[e];
-    } else {
-      const T* src = static_cast<const T*>(a.k) + (it.row + t) * a.k_stride + h * D;
-      load_lane<T, E>(src + j, x);
-      if (j < a.rot) {
+      for (int e = 0; e < E; ++e) {
+        c[e] = 1.f;
+        s[e] = 0.f;
+      }
+      if (turns) {
         const float* cs = rotation_row(a, it.pos + slot);
         if (a.interleaved) {
 #pragma unroll
           for (int e = 0; e < E; e += 2) {
-            const double c = cs[(j + e) / 2], s = cs[half + (j + e) / 2];
-            y[e] = static_cast<double>(x[e]) * c - static_cast<double>(x[e + 1]) * s;
-            y[e + 1] = static_cast<double>(x[e + 1]) * c + static_cast<double>(x[e]) * s;
+            c[e] = c[e + 1] = cs[angle + e / 2];
+            s[e] = s[e + 1] = cs[half + angle + e / 2];
           }
         } else {
-          const bool low = j < half;
-          const int jj = low ? j : j - half;
-          float z[E], c[E], s[E];
-          load_lane<T, E>(src + (low ? j + half : jj), z);
-          load_lane<float, E>(cs + jj, c);
-          load_lane<float, E>(cs + half + jj, s);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const double zs = static_cast<double>(z[e]) * static_cast<double>(s[e]);
-            y[e] = static_cast<double>(x[e]) * static_cast<double>(c[e]) + (low ? -zs : zs);
-          }
+          load_lane<float, E>(cs + angle, c);
+          load_lane<float, E>(cs + half + angle, s);
         }
-      } else {
+      }
+      if (a.interleaved) {  // the pair's other number
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = x[e];
+        for (int e = 0; e < E; e += 2) {
+          const float keep = z[e];
+          z[e] = z[e + 1];
+          z[e + 1] = keep;
+        }
+      }
+      // number e: x·c − z·s for the first of a pair, x·c + z·s for the second
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (a.interleaved ? (e & 1) == 0 : low) s[e] = -s[e];
+      float y[E], big = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        y[e] = fmaf(x[e], c[e], z[e] * s[e]);
+        big = fmaxf(big, fabsf(y[e]) + fabsf(z[e] * s[e]));
+      }
+      asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(big) : "f"(big));
+      uint32_t ksz, vsz;
+      const uint32_t kc = quantise_row<E>(
+          y, a.rot ? big * 0x1.1p-24f : 0.f,
+          [&](int e) {
+            return static_cast<double>(x[e]) * static_cast<double>(c[e]) +
+                   static_cast<double>(z[e]) * static_cast<double>(s[e]);
+          },
+          &ksz);
+      const uint32_t vc = quantise_row<E>(v, 0.f, [&](int e) { return static_cast<double>(v[e]); }, &vsz);
+      unsigned char* rec = page + (slot / kTile) * R;
+      const int r = slot % kTile;
+      if constexpr (E == 4) {
+        reinterpret_cast<uint16_t*>(rec + r * kRow)[lane] = static_cast<uint16_t>(kc);
+        reinterpret_cast<uint16_t*>(rec + (kTile + r) * kRow)[lane] = static_cast<uint16_t>(vc);
+        reinterpret_cast<uint16_t*>(codes_s + slot * kRow)[lane] = static_cast<uint16_t>(kc);
+      } else {
+        rec[r * kRow + lane] = static_cast<unsigned char>(kc);
+        rec[(kTile + r) * kRow + lane] = static_cast<unsigned char>(vc);
+        codes_s[slot * kRow + lane] = static_cast<unsigned char>(kc);
+      }
+      if (lane == 0) {
+        reinterpret_cast<uint32_t*>(rec + 16 * D)[r] = ksz;
+        reinterpret_cast<uint32_t*>(rec + 16 * D)[kTile + r] = vsz;
+        sz_s[slot] = ksz;
       }
     }
-    uint32_t sz;
-    const uint32_t codes = quantise_row<E>(y, &sz);
-    unsigned char* rec = page + (slot / kTile) * R;
-    const int r = slot % kTile;
-    unsigned char* to = rec + (isv * kTile + r) * kRow;
-    if constexpr (E == 4) {
-      reinterpret_cast<uint16_t*>(to)[lane] = static_cast<uint16_t>(codes);
-      if (!isv) reinterpret_cast<uint16_t*>(codes_s + slot * kRow)[lane] = static_cast<uint16_t>(codes);
-    } else {
-      to[lane] = static_cast<unsigned char>(codes);
-      if (!isv) codes_s[slot * kRow + lane] = static_cast<unsigned char>(codes);
+    if (a.box == nullptr) continue;
+    for (int i = threadIdx.x; i < it.lo * (kRow / 4); i += kThreads) {
+      const int slot = i / (kRow / 4), cc = i - slot * (kRow / 4);
+      reinterpret_cast<uint32_t*>(codes_s)[i] =
+          reinterpret_cast<const uint32_t*>(page + (slot / kTile) * R + (slot % kTile) * kRow)[cc];
     }
-    if (lane == 0) {
-      reinterpret_cast<uint32_t*>(rec + 16 * D)[isv * kTile + r] = sz;
-      if (!isv) sz_s[slot] = sz;
+    for (int slot = threadIdx.x; slot < it.lo; slot += kThreads)
+      sz_s[slot] = reinterpret_cast<const uint32_t*>(page + (slot / kTile) * R + 16 * D)[slot % kTile];
+    __syncthreads();
+    const int col = threadIdx.x;
+    if (col < D) {
+      float mx, mn;
+      double mean, var;
+      column_meta<S>(
+          [&](int t) { return q4_value(sz_s[t], (codes_s[t * kRow + col / 2] >> (4 * (col & 1))) & 15u); }, it.hi, &mx,
+          &mn, &mean, &var);
+      const size_t mh = (static_cast<size_t>(h) * a.num_phys + it.phys) * 2 * D + col;
+      bf16* box = static_cast<bf16*>(a.box);
+      bf16* mom = static_cast<bf16*>(a.mom);
+      box[mh] = bf16_away(mx, true);
+      box[mh + D] = bf16_away(mn, false);
+      mom[mh] = round_store<bf16>(mean);
+      mom[mh + D] = round_store<bf16>(var);
     }
+    if (h + 1 < h1) __syncthreads();  // the codes are read before the next head's enter
   }
-  if (a.box == nullptr) return;
-  for (int i = threadIdx.x; i < it.lo * (kRow / 4); i += kThreads) {
-    const int slot = i / (kRow / 4), c = i - slot * (kRow / 4);
-    reinterpret_cast<uint32_t*>(codes_s)[i] =
-        reinterpret_cast<const uint32_t*>(page + (slot / kTile) * R + (slot % kTile) * kRow)[c];
-  }
-  for (int slot = threadIdx.x; slot < it.lo; slot += kThreads)
-    sz_s[slot] = reinterpret_cast<const uint32_t*>(page + (slot / kTile) * R + 16 * D)[slot % kTile];
-  __syncthreads();
-  const int col = threadIdx.x;
-  if (col >= D) return;
-  float mx, mn;
-  double mean, var;
-  column_meta(
-      [&](int t) { return q4_value(sz_s[t], (codes_s[t * kRow + col / 2] >> (4 * (col & 1))) & 15u); }, it.hi, &mx,
-      &mn, &mean, &var);
-  const size_t mh = (static_cast<size_t>(h) * a.num_phys + it.phys) * 2 * D + col;
-  bf16* box = static_cast<bf16*>(a.box);
-  bf16* mom = static_cast<bf16*>(a.mom);
-  box[mh] = bf16_away(mx, true);
-  box[mh + D] = bf16_away(mn, false);
-  mom[mh] = round_store<bf16>(mean);
-  mom[mh + D] = round_store<bf16>(var);
 }
 
 struct ReadArgs {
@@ -405,34 +558,80 @@ struct ReadArgs {
   void* k_out;
   void* v_out;
   int batch, rows, Hkv, S, num_phys, max_pages;
+  int heads;  // KV heads that one CTA takes in turn
 };
 
-// grid: (items, Hkv); a thread turns eight codes (one word) into values.
+// grid: (items, CTAs of a.heads KV heads); a thread turns eight codes (one
+// word) of K and of V into values, two tokens of each at a time.  Bound by the
+// values' writes.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) q4_read_kernel(ReadArgs a) {
   grid_dep_enter();
   PageItem it;
   if (!page_item(a, blockIdx.x, &it)) return;
-  constexpr int R = q4_record_bytes(D), kWords = D / 8;
-  const int h = blockIdx.y, n = it.hi - it.lo;
-  const unsigned char* page = a.pool + (static_cast<size_t>(it.phys) * a.Hkv + h) * (a.S / kTile) * R;
-  for (int i = threadIdx.x; i < 2 * n * kWords; i += kThreads) {
-    const int row = i / kWords, w = i - row * kWords, isv = row >= n, t = isv ? row - n : row, slot = it.lo + t;
-    T* to = static_cast<T*>(isv ? a.v_out : a.k_out);
-    if (to == nullptr) continue;
-    const unsigned char* rec = page + (slot / kTile) * R;
-    const int r = isv * kTile + slot % kTile;
-    const uint32_t codes = reinterpret_cast<const uint32_t*>(rec + r * (D / 2))[w];
-    const uint32_t sz = reinterpret_cast<const uint32_t*>(rec + 16 * D)[r];
-    float v[8];
+  constexpr int R = q4_record_bytes(D), kWords = D / 8, kRows = kThreads / kWords;
+  const int w = threadIdx.x % kWords, n = it.hi - it.lo;
+  const int h1 = min(a.Hkv, (static_cast<int>(blockIdx.y) + 1) * a.heads);
+  for (int h = blockIdx.y * a.heads; h < h1; ++h) {
+    const unsigned char* page = a.pool + (static_cast<size_t>(it.phys) * a.Hkv + h) * (a.S / kTile) * R;
+    for (int t0 = threadIdx.x / kWords; t0 < n; t0 += 2 * kRows) {
+      uint32_t codes[2][2], sz[2][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = q4_value(sz, (codes >> (4 * e)) & 15u);
-    store8(to + (static_cast<int64_t>(it.row + t) * a.Hkv + h) * D + 8 * w, v);
+      for (int i = 0; i < 2; ++i) {
+        const int slot = it.lo + min(t0 + i * kRows, n - 1);
+        const unsigned char* rec = page + (slot / kTile) * R;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int r = v * kTile + slot % kTile;
+          codes[i][v] = reinterpret_cast<const uint32_t*>(rec + r * (D / 2))[w];
+          sz[i][v] = reinterpret_cast<const uint32_t*>(rec + 16 * D)[r];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int t = t0 + i * kRows;
+        if (t >= n) continue;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          T* to = static_cast<T*>(v ? a.v_out : a.k_out);
+          if (to == nullptr) continue;
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = q4_value(sz[i][v], (codes[i][v] >> (4 * e)) & 15u);
+          store8(to + (static_cast<int64_t>(it.row + t) * a.Hkv + h) * D + 8 * w, x);
+        }
+      }
+    }
   }
 }
 
 int item_count(const int32_t* indptr, int rows, int batch, int S) {
   return indptr == nullptr ? batch : rows / S + 2 * batch;
+}
+
+// KV heads per CTA: one while that gives the GPU at most four waves of five CTAs
+// per SM (a decode step, a short chunk: latency), else as many as keep four
+// (prompts: the page lookups cost 15 of 100 us with one head per CTA).
+int heads_per_cta(int items, int Hkv) {
+  const int64_t waves4 = 20ll * sm_count();
+  const int64_t h = static_cast<int64_t>(items) * Hkv / (waves4 > 0 ? waves4 : 1);
+  return static_cast<int>(h < 1 ? 1 : (h > Hkv ? Hkv : h));
+}
+
+template <typename T, int D>
+cudaError_t run_append(bool q4, int S, dim3 grid, cudaStream_t st, const AppendArgs& a) {
+  if (q4)
+    return launch_k(S == 16 ? rope_append_q4_kernel<T, D, 16> : rope_append_q4_kernel<T, D, 32>, grid, kThreads, 0, st, a);
+  return launch_k(S == 16 ? rope_append_kernel<T, D, 16> : rope_append_kernel<T, D, 32>, grid, kThreads, 0, st, a);
+}
+
+cudaError_t run_append(bool q4, int dtype, int d, const ekv_new_tokens& n, AppendArgs& a, cudaStream_t st) {
+  const int items = item_count(n.indptr, n.num_tokens, a.batch, a.S);
+  a.heads = heads_per_cta(items, a.Hkv);
+  const int per = (a.Hkv + a.heads - 1) / a.heads;
+  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(per * (n.q != nullptr ? 2 : 1)));
+  if (dtype == EKV_BF16) return d == 128 ? run_append<bf16, 128>(q4, a.S, grid, st, a) : run_append<bf16, 64>(q4, a.S, grid, st, a);
+  return d == 128 ? run_append<float, 128>(q4, a.S, grid, st, a) : run_append<float, 64>(q4, a.S, grid, st, a);
 }
 
 AppendArgs append_args(const ekv_seqs& s, const ekv_rope* rope, const ekv_new_tokens& n, int Hkv, int S,
@@ -473,12 +672,7 @@ cudaError_t launch_rope_append(const ekv_cache& c, const ekv_seqs& s, const ekv_
   a.v_pool = c.v_pool;
   a.box = c.box;
   a.mom = c.mom;
-  const int items = item_count(n.indptr, n.num_tokens, s.batch, c.page_size);
-  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(a.Hkv * (n.q != nullptr ? 2 : 1)));
-  const bool wide = c.head_dim == 128;
-  if (c.dtype == EKV_BF16)
-    return launch_k(wide ? rope_append_kernel<bf16, 128> : rope_append_kernel<bf16, 64>, grid, kThreads, 0, st, a);
-  return launch_k(wide ? rope_append_kernel<float, 128> : rope_append_kernel<float, 64>, grid, kThreads, 0, st, a);
+  return run_append(false, c.dtype, c.head_dim, n, a, st);
 }
 
 cudaError_t launch_rope_append_q4(const ekv_cache_q4& c, const ekv_seqs& s, const ekv_rope* rope,
@@ -487,23 +681,17 @@ cudaError_t launch_rope_append_q4(const ekv_cache_q4& c, const ekv_seqs& s, cons
   a.k_pool = c.pool;
   a.box = c.box;
   a.mom = c.mom;
-  const int items = item_count(n.indptr, n.num_tokens, s.batch, c.page_size);
-  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(a.Hkv * (n.q != nullptr ? 2 : 1)));
-  const bool wide = c.head_dim == 128;
-  if (n.dtype == EKV_BF16)
-    return launch_k(wide ? rope_append_q4_kernel<bf16, 128> : rope_append_q4_kernel<bf16, 64>, grid, kThreads, 0, st,
-                    a);
-  return launch_k(wide ? rope_append_q4_kernel<float, 128> : rope_append_q4_kernel<float, 64>, grid, kThreads, 0, st,
-                  a);
+  return run_append(true, n.dtype, c.head_dim, n, a, st);
 }
 
 cudaError_t launch_q4_read(const ekv_cache_q4& c, const ekv_seqs& s, const int32_t* indptr, int num_tokens,
                            int out_dtype, void* k_out, void* v_out, cudaStream_t st) {
   ReadArgs a{s.page_table, s.seq_lens,     indptr,      static_cast<const unsigned char*>(c.pool),
              k_out,        v_out,          s.batch,     num_tokens,
-             c.num_kv_heads, c.page_size,  c.num_phys_pages, s.max_pages};
-  const dim3 grid(static_cast<unsigned>(item_count(indptr, num_tokens, s.batch, c.page_size)),
-                  static_cast<unsigned>(c.num_kv_heads));
+             c.num_kv_heads, c.page_size,  c.num_phys_pages, s.max_pages, 1};
+  const int items = item_count(indptr, num_tokens, s.batch, c.page_size);
+  a.heads = heads_per_cta(items, c.num_kv_heads);
+  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>((c.num_kv_heads + a.heads - 1) / a.heads));
   const bool wide = c.head_dim == 128;
   if (out_dtype == EKV_BF16)
     return launch_k(wide ? q4_read_kernel<bf16, 128> : q4_read_kernel<bf16, 64>, grid, kThreads, 0, st, a);
