@@ -230,7 +230,7 @@ def make_cache_q4(pool, head_dim, box=None, mom=None) -> CacheQ4:
         raise ValueError("cache tensors must be contiguous")
     ptrs = [0 if t is None else t.data_ptr() for t in (pool, box, mom)]
     c = CacheQ4(head_dim, 16 * pool.shape[2], pool.shape[1], pool.shape[0], *ptrs)
-    c._keep, c.box_t, c.mom_t, c.device = keep, box, mom, pool.device
+    c._keep, c.box_t, c.mom_t, c.device_index = keep, box, mom, pool.get_device()
     if box is not None:
         c.meta = Cache(EKV_BF16, head_dim, c.page_size, c.num_kv_heads, c.num_phys_pages, ptrs[0], ptrs[0], *ptrs[1:])
         c.meta._keep, c.meta.box_t, c.meta.mom_t = keep, box, mom
@@ -242,7 +242,7 @@ def make_rope(cos_sin, interleaved=False) -> Rope:
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be contiguous fp32 [positions, rot_dim]")
     r = Rope(cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1], int(bool(interleaved)))
-    r._keep, r.device = cos_sin, cos_sin.device
+    r._keep, r.device_index = cos_sin, cos_sin.get_device()
     return r
 
 
@@ -268,7 +268,8 @@ def make_new_tokens(k, v, q=None, q_out=None, indptr=None) -> NewTokens:
     pq = (lambda t: 0 if t is None else t.data_ptr())
     n = NewTokens(pq(q), k.data_ptr(), v.data_ptr(), pq(q_out), 0 if q is None else q.stride(0), k.stride(0),
                   v.stride(0), pq(indptr), k.shape[0], 0 if q is None else q.shape[1], _DTYPES[k.dtype])
-    n._keep, n.device, n.shape = (rows, indptr), k.device, (k.shape[1], k.shape[2])
+    n._keep, n.device_index, n.heads = (rows, indptr), k.get_device(), (k.shape[1], k.shape[2])
+    n.sequences = None if indptr is None else indptr.numel() - 1
     return n
 
 
@@ -284,6 +285,12 @@ def make_score_mod(softcap=0.0, slopes=None, window=0, prefix_lens=None, starts=
     ptr = (lambda t: 0 if t is None else t.data_ptr())
     m = ScoreMod(float(softcap or 0.0), int(window or 0), ptr(slopes), ptr(prefix_lens), ptr(starts))
     m._keep = (slopes, prefix_lens, starts)
+    m.device_index = keep[0].get_device() if keep else None
+    m.query_heads = None if slopes is None else slopes.numel()
+    lens = {t.numel() for t in (prefix_lens, starts) if t is not None}
+    if len(lens) > 1:
+        raise ValueError("prefix_lens and starts must have one entry per sequence")
+    m.sequences = lens.pop() if lens else None
     return m
 
 
@@ -293,9 +300,10 @@ def _same_device(*tensors):
 
 
 def _on_current(device):
-    """Kernels launch on the current device: another one's tensors are refused."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {device}, which is not the current CUDA device")
+    """Kernels launch on the current device: another one's tensors (index −1: the
+    host's) are refused."""
+    if device < 0 or device != torch.cuda.current_device():
+        raise ValueError(f"tensors on device {device}, which is not the current CUDA device")
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
@@ -379,98 +387,123 @@ def ekv_decode_adaptive(cache, seqs, q, scale, alpha, k0, sel, n_sel, out, tau, 
     return int(k_used.value)
 
 
-def _check_append(cache_device, heads, seqs, rope, new):
-    _on_current(new.device)
-    if cache_device != new.device or (rope is not None and rope.device != new.device):
+def _raw_stream(stream, device):
+    """The cudaStream_t of a stream, or of the current one, as an int."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(device)
+    return torch.cuda.current_stream().cuda_stream
+
+
+# the current stream's handle without a Stream object around it (1 us less)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+# The serving calls run once per layer of a decode step, next to kernels of a few
+# microseconds: what can be checked once is checked where the descriptions are
+# made, and a call compares integers.
+def _check_append(device, heads, seqs, rope, new):
+    if new.device_index != device or (rope is not None and rope.device_index != device):
         raise ValueError("all tensors must be on one device")
-    if new.shape != heads:
-        raise ValueError(f"new tokens have [Hkv, d] = {new.shape}, the cache {heads}")
-    indptr = new._keep[1]
-    if indptr is not None and indptr.numel() != seqs.batch + 1:
+    _on_current(device)
+    if new.heads != heads:
+        raise ValueError(f"new tokens have [Hkv, d] = {new.heads}, the cache {heads}")
+    if new.sequences is not None and new.sequences != seqs.batch:
         raise ValueError("indptr must have batch + 1 entries")
 
 
 def ekv_rope_append(cache, seqs, rope, new, stream=None):
     """Rotate and append new tokens (rope None: no rotation); see include/ekv.h."""
-    _check_append(cache.box_t.device, (cache.num_kv_heads, cache.head_dim), seqs, rope, new)
-    _check("ekv_rope_append", lib().ekv_rope_append(
-        ctypes.byref(cache), ctypes.byref(seqs), None if rope is None else ctypes.byref(rope), ctypes.byref(new),
-        _stream(stream)))
+    device = cache.box_t.get_device()
+    _check_append(device, (cache.num_kv_heads, cache.head_dim), seqs, rope, new)
+    st = lib().ekv_rope_append(cache, seqs, rope, new, _raw_stream(stream, device))
+    if st:
+        raise EkvError("ekv_rope_append", st)
 
 
 def ekv_rope_append_q4(cache, seqs, rope, new, stream=None):
     """ekv_rope_append into a 4-bit cache."""
-    _check_append(cache.device, (cache.num_kv_heads, cache.head_dim), seqs, rope, new)
-    _check("ekv_rope_append_q4", lib().ekv_rope_append_q4(
-        ctypes.byref(cache), ctypes.byref(seqs), None if rope is None else ctypes.byref(rope), ctypes.byref(new),
-        _stream(stream)))
+    device = cache.device_index
+    _check_append(device, (cache.num_kv_heads, cache.head_dim), seqs, rope, new)
+    st = lib().ekv_rope_append_q4(cache, seqs, rope, new, _raw_stream(stream, device))
+    if st:
+        raise EkvError("ekv_rope_append_q4", st)
 
 
 def ekv_q4_read(cache, seqs, indptr, k_out=None, v_out=None, stream=None):
     """Read tokens of a 4-bit cache back as values.  k_out, v_out: fp32 or bf16
     [tokens, Hkv, d], dense, either None; indptr: int32 [batch + 1], the rows of
     each sequence's last tokens."""
-    outs = [t for t in (k_out, v_out) if t is not None]
-    if not outs:
+    out = k_out if k_out is not None else v_out
+    if out is None:
         raise ValueError("k_out or v_out is needed")
-    for t in outs:
-        if t.dtype not in _DTYPES or t.dtype != outs[0].dtype or not t.is_contiguous() or t.shape != outs[0].shape \
-                or tuple(t.shape[1:]) != (cache.num_kv_heads, cache.head_dim):
-            raise ValueError("k_out and v_out must be dense fp32 or bf16 [tokens, Hkv, d]")
-    if indptr.dtype != torch.int32 or not indptr.is_contiguous() or indptr.numel() != seqs.batch + 1:
+    shape, dt = out.shape, _DTYPES.get(out.dtype)
+    if dt is None or len(shape) != 3 or shape[1] != cache.num_kv_heads or shape[2] != cache.head_dim:
+        raise ValueError("k_out and v_out must be fp32 or bf16 [tokens, Hkv, d]")
+    if v_out is not None and (v_out.shape != shape or v_out.dtype != out.dtype):
+        raise ValueError("k_out and v_out must be alike")
+    if indptr.dtype != torch.int32 or indptr.numel() != seqs.batch + 1:
         raise ValueError("indptr must be int32 [batch + 1]")
-    _on_current(cache.device)
-    _same_device(indptr, *outs, cache._keep[0])
-    _check("ekv_q4_read", lib().ekv_q4_read(
-        ctypes.byref(cache), ctypes.byref(seqs), _ptr(indptr), outs[0].shape[0], _DTYPES[outs[0].dtype], _ptr(k_out),
-        _ptr(v_out), _stream(stream)))
+    device = cache.device_index
+    for t in (k_out, v_out, indptr):
+        if t is not None and not (t.is_contiguous() and t.get_device() == device):
+            raise ValueError("k_out, v_out and indptr must be dense, on the cache's device")
+    _on_current(device)
+    st = lib().ekv_q4_read(cache, seqs, indptr.data_ptr(), shape[0], dt, None if k_out is None else k_out.data_ptr(),
+                           None if v_out is None else v_out.data_ptr(), _raw_stream(stream, device))
+    if st:
+        raise EkvError("ekv_q4_read", st)
 
 
 def ekv_softmax_mod_workspace_bytes(head_dim, num_kv_heads, num_q_heads, num_q_tokens=1) -> int:
     return int(lib().ekv_softmax_mod_workspace_bytes(head_dim, num_kv_heads, num_q_heads, num_q_tokens))
 
 
-def _softmax_mod(name, cache, device, seqs, q, scale, mod, sel, n_sel, cap, out, ws, lse, stream):
-    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_contiguous():
-        raise ValueError("q must be dense bf16 [batch, T, Hq, d]")
-    if q.shape[0] != seqs.batch or q.shape[3] != cache.head_dim:
+def _softmax_mod(name, call, cache, device, seqs, q, scale, mod, sel, n_sel, cap, out, ws, lse, stream):
+    shape = q.shape
+    if len(shape) != 4 or q.dtype != torch.bfloat16:
+        raise ValueError("q must be bf16 [batch, T, Hq, d]")
+    batch, T, Hq, d = shape
+    if batch != seqs.batch or d != cache.head_dim:
         raise ValueError("q does not fit the batch and the cache")
-    if out.shape != q.shape or out.dtype != torch.float32 or not out.is_contiguous():
-        raise ValueError("out must be dense fp32 of q's shape")
-    if lse is not None and (lse.shape != q.shape[:3] or lse.dtype != torch.float32 or not lse.is_contiguous()):
-        raise ValueError("lse must be dense fp32 [batch, T, Hq]")
-    if sel is not None and (sel.dtype != torch.int32 or not sel.is_contiguous()
-                            or tuple(sel.shape) != (seqs.batch, cache.num_kv_heads, cap)):
-        raise ValueError("sel must be dense int32 [batch, Hkv, cap]")
-    if n_sel is not None and (n_sel.dtype != torch.int32 or n_sel.numel() != seqs.batch * cache.num_kv_heads
-                              or not n_sel.is_contiguous()):
-        raise ValueError("n_sel must be dense int32 [batch, Hkv]")
+    if out.shape != shape or out.dtype != torch.float32:
+        raise ValueError("out must be fp32 of q's shape")
+    if lse is not None and (lse.shape != shape[:3] or lse.dtype != torch.float32):
+        raise ValueError("lse must be fp32 [batch, T, Hq]")
+    if sel is not None and (sel.dtype != torch.int32 or tuple(sel.shape) != (batch, cache.num_kv_heads, cap)):
+        raise ValueError("sel must be int32 [batch, Hkv, cap]")
+    if n_sel is not None and (n_sel.dtype != torch.int32 or n_sel.numel() != batch * cache.num_kv_heads):
+        raise ValueError("n_sel must be int32 [batch, Hkv]")
+    for t in (q, out, ws, lse, sel, n_sel):
+        if t is not None and not (t.is_contiguous() and t.get_device() == device):
+            raise ValueError("q, out, lse, sel, n_sel and ws must be dense, on the cache's device")
     if mod is not None:
-        slopes, prefix_lens, starts = mod._keep
-        if slopes is not None and slopes.numel() != q.shape[2]:
+        if mod.query_heads not in (None, Hq):
             raise ValueError("slopes must have one entry per query head")
-        if any(t is not None and t.numel() != seqs.batch for t in (prefix_lens, starts)):
+        if mod.sequences not in (None, batch):
             raise ValueError("prefix_lens and starts must have one entry per sequence")
+        if mod.device_index not in (None, device):
+            raise ValueError("all tensors must be on one device")
     _on_current(device)
-    _same_device(cache._keep[0], q, out, ws, *(t for t in (lse, sel, n_sel) if t is not None),
-                 *(t for t in (mod._keep if mod is not None else ()) if t is not None))
-    _check(name, getattr(lib(), name)(
-        ctypes.byref(cache), ctypes.byref(seqs), _ptr(q), q.shape[2], q.shape[1], scale,
-        None if mod is None else ctypes.byref(mod), _ptr(sel), _ptr(n_sel), cap, _ptr(out), _ptr(lse), _ptr(ws),
-        ws.numel(), _stream(stream)))
+    st = call(cache, seqs, q.data_ptr(), Hq, T, scale, mod, None if sel is None else sel.data_ptr(),
+              None if n_sel is None else n_sel.data_ptr(), cap, out.data_ptr(), None if lse is None else lse.data_ptr(),
+              ws.data_ptr(), ws.numel(), _raw_stream(stream, device))
+    if st:
+        raise EkvError(name, st)
 
 
 def ekv_softmax_decode_mod(cache, seqs, q, scale, mod, sel, n_sel, cap, out, ws, *, lse=None, stream=None):
     """Softmax decode with capped, biased and masked scores (mod: make_score_mod,
     or None) for the last T tokens of every sequence.  q: bf16 [B, T, Hq, d]."""
-    _softmax_mod("ekv_softmax_decode_mod", cache, cache.box_t.device, seqs, q, scale, mod, sel, n_sel, cap, out, ws,
-                 lse, stream)
+    _softmax_mod("ekv_softmax_decode_mod", lib().ekv_softmax_decode_mod, cache, cache.box_t.get_device(), seqs, q, scale,
+                 mod, sel, n_sel, cap, out, ws, lse, stream)
 
 
 def ekv_softmax_decode_q4(cache, seqs, q, scale, mod, sel, n_sel, cap, out, ws, *, lse=None, stream=None):
     """ekv_softmax_decode_mod over a 4-bit cache."""
-    _softmax_mod("ekv_softmax_decode_q4", cache, cache.device, seqs, q, scale, mod, sel, n_sel, cap, out, ws, lse,
-                 stream)
+    _softmax_mod("ekv_softmax_decode_q4", lib().ekv_softmax_decode_q4, cache, cache.device_index, seqs, q, scale, mod, sel,
+                 n_sel, cap, out, ws, lse, stream)
 
 
 def ekv_selftest_wait_timeout(polls=1024, stream=None):

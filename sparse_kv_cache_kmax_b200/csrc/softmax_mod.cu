@@ -25,6 +25,8 @@
 // The bound is HBM: 512 bytes per bf16 (token, KV head), 136 in 4 bits.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "q4.cuh"
 
 namespace ekv {
@@ -1270,9 +1272,17 @@ inline size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 template <int D, int NT, int R, bool Q4>
 cudaError_t run_mod(const ModArgs& a, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t st) {
   constexpr size_t smem = mod_smem<D, NT, R, Q4>();
-  cudaError_t e = cudaFuncSetAttribute(mod_kernel<D, NT, R, Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<uint64_t> ready{0};  // devices on which the kernel may have that much shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(mod_kernel<D, NT, R, Q4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   const int ctas = min(kModCtas, 2 * sm_count());
   e = launch_k(mod_kernel<D, NT, R, Q4>, dim3(static_cast<unsigned>(ctas)), Shape<D, NT, Q4>::threads, smem, st, km, vm, a);
   if (e != cudaSuccess) return e;
