@@ -151,6 +151,12 @@ __device__ __forceinline__ int group_tiles(const ModArgs& a, int grp) {
   return max(1, max(0, min(a.n_sel[grp], a.cap)) * (a.S / kTile));
 }
 
+// Pieces of about 1/inv tiles that a unit of n tiles is cut into: at least one,
+// at most n, the same for everybody who asks.
+__device__ __forceinline__ int piece_count(int n, float inv) {
+  return min(n, 1 + static_cast<int>(static_cast<float>(n - 1) * inv));
+}
+
 // The part of a unit that a CTA works on: tiles t0 .. t1−1 of n, one of
 // `pieces` parts (the first one of them knows how many).
 struct Segment {
@@ -284,6 +290,10 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
     mbar_init(&bars[tid], 1);
     fence_mbar_init();
   }
+  if (!Q4 && tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&kmap) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&vmap) : "memory");
+  }
   grid_dep_enter();
 
   // This CTA's run of the work list.  Cutting the list into equal runs keeps
@@ -314,14 +324,20 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   };
   const long long total = sum_over_groups([](int n) { return n; });
   const int ctas = static_cast<int>(gridDim.x);
-  int per = max(static_cast<int>((total + ctas - 1) / ctas), a.min_tiles);
+  int per = total < 0x70000000 ? static_cast<int>((static_cast<uint32_t>(total) + ctas - 1) / static_cast<uint32_t>(ctas))
+                               : static_cast<int>((total + ctas - 1) / ctas);
+  per = max(per, a.min_tiles);
   bool aligned = false;
   if (static_cast<long long>(groups) * mult <= ctas) {
-    auto pieces = [&](int by) { return sum_over_groups([by](int n) { return (n + by - 1) / by; }); };
+    auto pieces = [&](int by) {
+      const float inv = 1.f / static_cast<float>(by);
+      return sum_over_groups([inv](int n) { return n > 0 ? piece_count(n, inv) : 0; });
+    };
     aligned = pieces(per) <= ctas;
     if (!aligned) {
       // equal units: what the CTAs of one would take
-      const int units = groups * mult, each = ctas / units, by = (static_cast<int>(total / units) + each - 1) / each;
+      const uint32_t units = static_cast<uint32_t>(groups * mult), each = ctas / units;
+      const int by = static_cast<int>((static_cast<uint32_t>(total / units) + each - 1) / each);
       if (by >= per && by - per <= a.slack_tiles && pieces(by) <= ctas) {
         aligned = true;
         per = by;
@@ -331,6 +347,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   if (tid == 0) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
   // the group that holds this CTA's start: counted in pieces, or in tiles
   const long long start = aligned ? blockIdx.x : static_cast<long long>(per) * blockIdx.x;
+  const float inv_per = 1.f / static_cast<float>(per);
   long long pos = start, grp_at = 0;
   int grp = -1, grp_tiles = 0;
   for (int c0 = 0; c0 < groups && grp < 0; c0 += 128) {
@@ -338,7 +355,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
     int len[4], x = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      len[i] = (aligned ? (mine[i] + per - 1) / per : mine[i]) * mult;
+      len[i] = (aligned && mine[i] > 0 ? piece_count(mine[i], inv_per) : mine[i]) * mult;
       x += len[i];
     }
     int up = x;  // inclusive scan over the lanes
@@ -375,18 +392,21 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   seg.vis = visible_tiles(a, a.sel ? grp / a.Hkv : grp);
   seg.n = grp_tiles;
   auto place = [&]() {  // the unit at pos of group grp
-    const int off = static_cast<int>(pos - grp_at);
+    const uint32_t off = static_cast<uint32_t>(pos - grp_at);
     seg.b = a.sel ? grp / a.Hkv : grp;
     int hh;
     if (aligned) {
-      const int np = (seg.n + per - 1) / per, piece = off % np;
-      hh = off / np;
-      seg.t0 = static_cast<int>(static_cast<long long>(seg.n) * piece / np);
-      seg.t1 = static_cast<int>(static_cast<long long>(seg.n) * (piece + 1) / np);
-      seg.pieces = np;
+      // pieces of equal length, the first n mod np of them one longer
+      const uint32_t np = static_cast<uint32_t>(piece_count(seg.n, inv_per)), unit = off / np;
+      const int piece = static_cast<int>(off - unit * np), each = static_cast<int>(seg.n / np);
+      const int more = seg.n - each * static_cast<int>(np);
+      hh = static_cast<int>(unit);
+      seg.t0 = piece * each + min(piece, more);
+      seg.t1 = seg.t0 + each + (piece < more ? 1 : 0);
+      seg.pieces = static_cast<int>(np);
     } else {
-      hh = off / seg.n;
-      seg.t0 = off - hh * seg.n;
+      hh = static_cast<int>(off / static_cast<uint32_t>(seg.n));
+      seg.t0 = static_cast<int>(off) - hh * seg.n;
       const long long left = end - pos;
       seg.t1 = left < seg.n - seg.t0 ? seg.t0 + static_cast<int>(left) : seg.n;
       seg.pieces = static_cast<int>((pos - seg.t0 + seg.n - 1) / per) - static_cast<int>(blockIdx.x) + 1;
@@ -740,25 +760,32 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
               all &= v;
             }
           const uint32_t seen = __ballot_sync(0xffffffffu, any && lane < kTile);
-          uint32_t some = seen & ~__ballot_sync(0xffffffffu, all && lane < kTile);
-          unsigned char* vt = buf + D / 64 * kTile * 128;
-          for (uint32_t rest = ~seen & 0xffffu; rest; rest &= rest - 1) {
-            const int tok = __ffs(rest) - 1;
-            if (lane < D / 8)
-              *reinterpret_cast<uint4*>(vt + (lane >> 3) * (kTile * 128) + tok * 128 + (lane & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-          }
-          for (; some; some &= some - 1) {
-            const int tok = __ffs(some) - 1;
-            bool bad = false;
-            if (lane < D / 8) {
-              const uint4 x = *reinterpret_cast<const uint4*>(vt + (lane >> 3) * (kTile * 128) + tok * 128 + (lane & 7) * 16);
-              const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+          const uint32_t some = seen & ~__ballot_sync(0xffffffffu, all && lane < kTile);
+          // lane: half a row (D/16 chunks of 16 bytes) of token lane/2
+          const int tok = lane >> 1;
+          unsigned char* row = buf + D / 64 * kTile * 128 + tok * 128;
+          auto chunk = [&](int i) {
+            const int c = (lane & 1) * (D / 16) + i;
+            return reinterpret_cast<uint4*>(row + (c >> 3) * (kTile * 128) + (c & 7) * 16);
+          };
+          if (!(seen >> tok & 1u)) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                bad |= (xs[i] & 0x7f80u) == 0x7f80u || (xs[i] & 0x7f800000u) == 0x7f800000u;
+            for (int i = 0; i < D / 16; ++i) *chunk(i) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          if (some) {
+            bool bad = false;
+            if (some >> tok & 1u) {
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const uint4 x = *chunk(i);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  bad |= (xs[e] & 0x7f80u) == 0x7f80u || (xs[e] & 0x7f800000u) == 0x7f800000u;
+              }
             }
-            if (__any_sync(0xffffffffu, bad)) apart |= 1u << tok;
+            const uint32_t lanes = __ballot_sync(0xffffffffu, bad);
+            for (uint32_t rest = lanes; rest; rest &= rest - 1) apart |= 1u << ((__ffs(rest) - 1) >> 1);
           }
           __syncwarp();
         }
@@ -1183,66 +1210,85 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   }
 }
 
-// grid (CTAs of mod_kernel, rows), D threads × 4 slices of the pieces: adds the
-// pieces of the unit that CTA x cut, in CTA order.  What bounds it is the chain
-// of dependent loads, so the first pieces are read before their weights are known.
+// grid (CTAs of mod_kernel, blocks of kMerge/(D/4) rows): adds the pieces of the
+// unit that CTA x cut, in CTA order.  A thread takes four numbers of a row over
+// every slices-th piece (one slice where the rows fill the block), eight pieces'
+// loads at a time: the chain of dependent loads is what bounds it, and one block
+// per CTA for up to 16 rows keeps it to one wave.
+constexpr int kMerge = 512;
 template <int D>
-__global__ void __launch_bounds__(4 * D) mod_combine_kernel(ModArgs a) {
+__global__ void __launch_bounds__(kMerge) mod_combine_kernel(ModArgs a) {
   grid_dep_enter();
   const int4 cut = a.cut[blockIdx.x];
   if (cut.z <= 1) return;
   constexpr int kAhead = 8;
-  __shared__ float s_num[4][D];
-  const int rows = a.G * a.T, row = blockIdx.y, c = threadIdx.x % D, sl = threadIdx.x / D, lane = threadIdx.x & 31;
+  __shared__ float4 s_num[kMerge];
+  __shared__ float2 s_ml[kMerge];
+  const int rows = a.G * a.T, items = rows * (D / 4);
+  const int slices = items < kMerge ? kMerge / items : 1;
+  const int sl = items < kMerge ? static_cast<int>(threadIdx.x) / items : 0;
+  const int item = blockIdx.y * kMerge + threadIdx.x - sl * items;
+  const bool live = sl < slices && item < items;
+  const int row = live ? item / (D / 4) : 0, c = (item % (D / 4)) * 4, cta = blockIdx.x, n = cut.z;
   const int b = cut.x / a.Hkv, h = cut.x - b * a.Hkv, t = row / a.G, hq = h * a.G + row - t * a.G;
-  const int cta = blockIdx.x, n = cut.z;
   auto slot = [&](int p) { return static_cast<size_t>(p == 0 ? cut.y : 2 * (cta + p)); };
-  float early[kAhead];
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) early[i] = a.part[(slot(min(sl + 4 * i, n - 1)) * rows + row) * D + c];
   float slope = 0.f;
-  int qpos = 0;
+  int qpos = 0, base = 0;
   if (a.slopes) {
     slope = a.slopes[hq];
     const int L = a.seq_lens[b], most = a.max_pages * a.S;
     qpos = (L < 0 ? 0 : (L > most ? most : L)) - a.T + t;
+    // the pieces' biases are measured from distances of their own: all to the
+    // last piece's (the nearest tokens), or the first's for a rising bias
+    base = ref_distance(slope, qpos, a.ref[slot(slope >= 0.f ? n - 1 : 0)]);
   }
-  // the pieces' biases are measured from distances of their own: all to the
-  // last piece's (the nearest tokens), or the first's for a rising bias
-  const int base = a.slopes ? ref_distance(slope, qpos, a.ref[slot(slope >= 0.f ? n - 1 : 0)]) : 0;
-  auto top_of = [&](int p, float m) {
-    return a.slopes ? m - slope * kLog2e * static_cast<float>(ref_distance(slope, qpos, a.ref[slot(p)]) - base) : m;
+  float m = -INFINITY, den = 0.f;
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float m2, float den2, float4 x) {
+    const float up = fmaxf(m, m2);
+    const float f = m > -INFINITY ? ex2(m - up) : 0.f, f2 = m2 > -INFINITY ? ex2(m2 - up) : 0.f;
+    den = den * f + den2 * f2;
+    num = make_float4(fmaf(num.x, f, x.x * f2), fmaf(num.y, f, x.y * f2), fmaf(num.z, f, x.z * f2),
+                      fmaf(num.w, f, x.w * f2));
+    m = up;
   };
-  // every warp: all pieces' maxima and sums, one piece per lane
-  float top = -INFINITY, den = 0.f;
-  for (int p = lane; p < n; p += 32) {
-    const float2 x = a.ml[slot(p) * rows + row];
-    const float m = top_of(p, x.x), up = fmaxf(top, m);
-    if (up > -INFINITY) den = den * ex2(top - up) + x.y * ex2(m - up);
-    else den += x.y;
-    top = up;
-  }
-  const float all = warp_max(top);
-  den = warp_sum(all > -INFINITY ? den * ex2(top - all) : den);
-  float num = 0.f;
-  auto add = [&](int p, float x) {
-    const float m = top_of(p, a.ml[slot(p) * rows + row].x);
-    num = fmaf(x, m > -INFINITY ? ex2(m - all) : 0.f, num);
-  };
+  if (live) {
+    for (int p0 = sl; p0 < n; p0 += kAhead * slices) {
+      float4 x[kAhead];
+      float2 ml[kAhead];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (sl + 4 * i < n) add(sl + 4 * i, early[i]);
-#pragma unroll 4
-  for (int p = sl + 4 * kAhead; p < n; p += 4) add(p, a.part[(slot(p) * rows + row) * D + c]);
-  s_num[sl][c] = num;
-  __syncthreads();
-  if (sl != 0) return;
-  num = s_num[0][c] + s_num[1][c] + s_num[2][c] + s_num[3][c];
+      for (int i = 0; i < kAhead; ++i) {
+        const size_t at = slot(min(p0 + i * slices, n - 1)) * rows + row;
+        x[i] = *reinterpret_cast<const float4*>(a.part + at * D + c);
+        ml[i] = a.ml[at];
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int p = p0 + i * slices;
+        if (p >= n) break;
+        float top = ml[i].x;
+        if (a.slopes) top -= slope * kLog2e * static_cast<float>(ref_distance(slope, qpos, a.ref[slot(p)]) - base);
+        add(top, ml[i].y, x[i]);
+      }
+    }
+  }
+  if (slices > 1) {
+    s_num[threadIdx.x] = num;
+    s_ml[threadIdx.x] = make_float2(m, den);
+    __syncthreads();
+    if (sl != 0) return;
+    for (int k = 1; k < slices; ++k) {
+      const float2 ml = s_ml[threadIdx.x + k * items];
+      add(ml.x, ml.y, s_num[threadIdx.x + k * items]);
+    }
+  }
+  if (!live) return;
   const size_t orow = (static_cast<size_t>(b) * a.T + t) * a.Hq + hq;
-  const bool none = all == -INFINITY && den == den;
-  a.out[orow * D + c] = none ? 0.f : num / den;
-  if (c == 0 && a.lse)
-    a.lse[orow] = none ? -INFINITY : (all + log2f(den)) * kLn2 - slope * static_cast<float>(base);
+  const bool none = m == -INFINITY && den == den;
+  const float by = 1.f / den;
+  *reinterpret_cast<float4*>(a.out + orow * D + c) =
+      none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(num.x * by, num.y * by, num.z * by, num.w * by);
+  if (c == 0 && a.lse) a.lse[orow] = none ? -INFINITY : (m + log2f(den)) * kLn2 - slope * static_cast<float>(base);
 }
 
 // Two-dimensional view [rows, d] of a pool, copied 16 rows × 64 columns at a
@@ -1286,8 +1332,9 @@ cudaError_t run_mod(const ModArgs& a, const CUtensorMap& km, const CUtensorMap& 
   const int ctas = min(kModCtas, 2 * sm_count());
   e = launch_k(mod_kernel<D, NT, R, Q4>, dim3(static_cast<unsigned>(ctas)), Shape<D, NT, Q4>::threads, smem, st, km, vm, a);
   if (e != cudaSuccess) return e;
-  return launch_k(mod_combine_kernel<D>, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(a.G * a.T)), 4 * D, 0,
-                  st, a);
+  const int items = a.G * a.T * (D / 4);
+  return launch_k(mod_combine_kernel<D>, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>((items + kMerge - 1) / kMerge)),
+                  kMerge, 0, st, a);
 }
 
 template <int D, bool Q4>
