@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
     int2 ref = make_int2(0, 0);
     if (a.slopes) ref = make_int2(tile_position(a, now, now.t0), tile_position(a, now, now.t1 - 1) + kTile - 1);
     uint32_t qf[kSharedQ ? 1 : KS][NT][2];
-    float qsum[NT][2], qdown[NT][2], qc[NT][2];  // 4 bits, the lane's columns: (Σ q)·factor, factor/2^k, −8·Σ q·2^k
+    float qsum[NT][2], qdown[NT][2], qc[NT][4];  // 4 bits, the lane's columns: (Σ q)·factor, factor/2^k, −8·Σ q·2^k (twice)
     auto row_position = [&](int nt, int e) {
       const int row = (rg * NT + nt) * 8 + 2 * t4 + e;
       return now.vis.L - a.T + (row < rows ? row : 0) / a.G;
@@ -578,8 +578,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
         qsum[nt][0] = __shfl_sync(0xffffffffu, sum * zf, 8 * t4);
         qsum[nt][1] = __shfl_sync(0xffffffffu, sum * zf, 8 * t4 + 4);
         const float c8 = sum * up * -0x1p-65f * 0x1p-65f;
-        qc[nt][0] = __shfl_sync(0xffffffffu, c8, 8 * t4);
-        qc[nt][1] = __shfl_sync(0xffffffffu, c8, 8 * t4 + 4);
+        qc[nt][0] = qc[nt][2] = __shfl_sync(0xffffffffu, c8, 8 * t4);
+        qc[nt][1] = qc[nt][3] = __shfl_sync(0xffffffffu, c8, 8 * t4 + 4);
         qdown[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t4);
         qdown[nt][1] = __shfl_sync(0xffffffffu, down, 8 * t4 + 4);
       }
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 // from −8·Σ q: the sum is of n − 8, which keeps it small
-                if (w + b == 0) mma(z[u][nt], af, bq[nt], qc[nt][0], qc[nt][1], qc[nt][0], qc[nt][1]);
+                if (w + b == 0) mma(z[u][nt], af, bq[nt], qc[nt]);
                 else mma(z[u][nt], af, bq[nt], z[u][nt]);
               }
             }
@@ -1045,45 +1045,54 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
               un[u][hf][2 * w + 1] = __byte_perm(wv[2 * hf][w], wv[2 * hf + 1][w], 0x7632);
             }
         }
-        constexpr int JB = 2;  // independent products in flight: JB·NT
+        // Rows in two sets, so that the four registers an offset needs are filled
+        // once for each: even j (codes in the lower places), then odd j.
+        constexpr int JB = 2;  // independent products in flight: U·JB·NT
 #pragma unroll
-        for (int j0v = 0; j0v < MT; j0v += JB) {
-          uint32_t af[U][JB][4];
-          float t[U][JB][NT][4];
+        for (int odd = 0; odd < 2; ++odd) {
+          float c[U][NT][4];
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int jj = 0; jj < JB; ++jj) {
-              // m rows g: number j of the lane's share; rows g + 8: number MT + j
-              const int j = j0v + jj;
-              const uint32_t mask = j & 1 ? 0x00f000f0u : 0x000f000fu;
-              af[u][jj][0] = (un[u][0][j / 4] >> (8 * (j >> 1 & 1))) & mask;
-              af[u][jj][1] = (un[u][0][MT / 4 + j / 4] >> (8 * (j >> 1 & 1))) & mask;
-              af[u][jj][2] = (un[u][1][j / 4] >> (8 * (j >> 1 & 1))) & mask;
-              af[u][jj][3] = (un[u][1][MT / 4 + j / 4] >> (8 * (j >> 1 & 1))) & mask;
-            }
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int part = 0; part < 3; ++part)
+              for (int e = 0; e < 4; ++e) c[u][nt][e] = c8[u][nt][e & 1] * (odd ? 16.f : 1.f);
+#pragma unroll
+          for (int q = 0; q < MT / 2; q += JB) {
+            uint32_t af[U][JB][4];
+            float t[U][JB][NT][4];
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-              for (int jj = 0; jj < JB; ++jj)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  const float by = (j0v + jj) & 1 ? 16.f : 1.f, a0 = c8[u][nt][0] * by, a1 = c8[u][nt][1] * by;
-                  if (part == 0) mma(t[u][jj][nt], af[u][jj], pf[u][nt][part], a0, a1, a0, a1);
-                  else mma(t[u][jj][nt], af[u][jj], pf[u][nt][part], t[u][jj][nt]);
-                }
-#pragma unroll
-          for (int jj = 0; jj < JB; ++jj)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float sum = t[0][jj][nt][e];
-                if constexpr (U == 2) sum += t[U - 1][jj][nt][e];
-                o[j0v + jj][nt][e] += sum;
+              for (int jj = 0; jj < JB; ++jj) {
+                // m rows g: number j of the lane's share; rows g + 8: number MT + j
+                const int j = 2 * (q + jj) + odd, sh = 8 * (j >> 1 & 1);
+                const uint32_t mask = odd ? 0x00f000f0u : 0x000f000fu;
+                af[u][jj][0] = (un[u][0][j / 4] >> sh) & mask;
+                af[u][jj][1] = (un[u][0][MT / 4 + j / 4] >> sh) & mask;
+                af[u][jj][2] = (un[u][1][j / 4] >> sh) & mask;
+                af[u][jj][3] = (un[u][1][MT / 4 + j / 4] >> sh) & mask;
               }
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+#pragma unroll
+              for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int jj = 0; jj < JB; ++jj)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt)
+                    mma(t[u][jj][nt], af[u][jj], pf[u][nt][part], part == 0 ? c[u][nt] : t[u][jj][nt]);
+#pragma unroll
+            for (int jj = 0; jj < JB; ++jj)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float sum = t[0][jj][nt][e];
+                  if constexpr (U == 2) sum += t[U - 1][jj][nt][e];
+                  o[2 * (q + jj) + odd][nt][e] += sum;
+                }
+          }
         }
       }
       // the slot is free: the next copies into it
