@@ -49,30 +49,45 @@ struct PageItem {
 // Called by whole warps; every lane gets the same answer.
 template <class A>
 __device__ bool page_item(const A& a, int item, PageItem* out) {
-  int b = item, row0 = item, n = 1, k = 0;
+  int b = item, row0 = item, n = 1, k = 0, L;
   if (a.indptr != nullptr) {
-    // greatest b with base(b) ≤ item, 32 probes at a time
+    // greatest b with base(b) ≤ item, 32 probes at a time; the last probes bring
+    // the sequence's rows and length along, so that two dependent loads (these,
+    // and the page table's) lead to the page
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) >> 5;
-      const int at = lo + lane * step;
-      const bool le = at < hi && a.indptr[at] / a.S + 2 * at <= item;
-      const int c = __popc(__ballot_sync(0xffffffffu, le || lane == 0));
-      lo += (c - 1) * step;
+    for (;;) {
+      const int step = (hi - lo + 31) >> 5, at = lo + lane * step;
+      int first = 0, end = 0, len = 0;
+      if (at < hi) {
+        first = a.indptr[at];
+        if (step == 1) {
+          end = a.indptr[at + 1];
+          len = a.seq_lens[at];
+        }
+      }
+      const bool le = at < hi && first / a.S + 2 * at <= item;
+      const int c = __popc(__ballot_sync(0xffffffffu, le || lane == 0)) - 1;
+      lo += c * step;
+      if (step == 1) {
+        b = lo;
+        row0 = __shfl_sync(0xffffffffu, first, c);
+        n = __shfl_sync(0xffffffffu, end, c);
+        L = __shfl_sync(0xffffffffu, len, c);
+        break;
+      }
       hi = min(hi, lo + step);
     }
-    b = lo;
-    row0 = a.indptr[b];
-    const int end = a.indptr[b + 1];
+    const int end = n;
     n = end - row0;
     k = item - (row0 / a.S + 2 * b);
     if (row0 < 0 || n < 0 || end > a.rows) {
       raise_flag(EKV_EFLAG_BAD_LEN);
       return false;
     }
+  } else {
+    L = a.seq_lens[b];
   }
-  const int L = a.seq_lens[b];
   if (n == 0 || (a.indptr == nullptr && L == 0)) return false;
   if (L < n || L > a.max_pages * a.S) {
     raise_flag(EKV_EFLAG_BAD_LEN);
@@ -232,16 +247,22 @@ __device__ void rotate_queries(const AppendArgs& a, const PageItem& it, int h0, 
     const T* src = static_cast<const T*>(a.q) + row * a.q_stride;
     T* dst = static_cast<T*>(a.q_out) + static_cast<int64_t>(row) * Hq * D;
     constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
-    for (int hq = first; hq < last; hq += kAhead * heads) {
+    int hq = first;
+    for (; hq + (kAhead - 1) * heads < last; hq += kAhead * heads) {
       Raw<T> raw[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
-        load_raw<T>(raw[i], src + static_cast<int64_t>(min(hq + i * heads, last - 1)) * D, l.u, a.rot, a.interleaved);
+        load_raw<T>(raw[i], src + static_cast<int64_t>(hq + i * heads) * D, l.u, a.rot, a.interleaved);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
-        if (hq + i * heads < last)
-          rotate_unit<T>(raw[i], turn, dst + static_cast<int64_t>(hq + i * heads) * D, static_cast<T*>(nullptr), l.u,
-                         a.rot, a.interleaved);
+        rotate_unit<T>(raw[i], turn, dst + static_cast<int64_t>(hq + i * heads) * D, static_cast<T*>(nullptr), l.u,
+                       a.rot, a.interleaved);
+    }
+    for (; hq < last; hq += heads) {
+      Raw<T> raw;
+      load_raw<T>(raw, src + static_cast<int64_t>(hq) * D, l.u, a.rot, a.interleaved);
+      rotate_unit<T>(raw, turn, dst + static_cast<int64_t>(hq) * D, static_cast<T*>(nullptr), l.u, a.rot,
+                     a.interleaved);
     }
   }
 }
@@ -265,7 +286,10 @@ __device__ __forceinline__ void column_meta(F value, int n, float* mx, float* mn
       s = __dadd_rn(s, static_cast<double>(x[t]));
     }
   }
-  const double dn = static_cast<double>(n), m = __ddiv_rn(s, dn);
+  // a full page's n is a power of two: its quotients are products, bit for bit,
+  // without the division's long chain
+  const double dn = static_cast<double>(n), by = 1.0 / P;
+  const double m = n == P ? __dmul_rn(s, by) : __ddiv_rn(s, dn);
 #pragma unroll
   for (int t = 0; t < P; ++t) {
     if (t < n) {
@@ -276,7 +300,7 @@ __device__ __forceinline__ void column_meta(F value, int n, float* mx, float* mn
   *mx = hi;
   *mn = lo;
   *mean = m;
-  *var = __ddiv_rn(v, dn);
+  *var = n == P ? __dmul_rn(v, by) : __ddiv_rn(v, dn);
 }
 
 // grid: (items, CTAs for K and V, then as many for the queries); a CTA takes
@@ -298,24 +322,27 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(AppendArgs a) 
   constexpr int kChunk = 16 / sizeof(T), kChunks = D / kChunk, kRows = kThreads / kChunks, kPasses = S / kRows;
   const Layout l = row_layout(D, a.rot, a.interleaved);
   const int vrow = threadIdx.x / kChunks, vcol = (threadIdx.x % kChunks) * kChunk;
+  const bool mine = l.u < l.units && l.r0 < n;
+  uint4 v[kPasses];
+  Raw<T> raw;  // the thread's first row of K
+  const T* ksrc = static_cast<const T*>(a.k) + static_cast<int64_t>(it.row) * a.k_stride;
+  const T* vsrc = static_cast<const T*>(a.v) + static_cast<int64_t>(it.row) * a.v_stride + vcol;
+  auto load = [&](int h) {
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+      v[i] = *reinterpret_cast<const uint4*>(vsrc + min(vrow + i * kRows, n - 1) * a.v_stride + h * D);
+    if (mine) load_raw<T>(raw, ksrc + l.r0 * a.k_stride + h * D, l.u, a.rot, a.interleaved);
+  };
+  load(h0);
   for (int h = h0; h < h1; ++h) {
     const size_t ph = static_cast<size_t>(it.phys) * a.Hkv + h;
     T* kp = static_cast<T*>(a.k_pool) + ph * S * D;
     T* vp = static_cast<T*>(a.v_pool) + ph * S * D;
-    const T* vsrc = static_cast<const T*>(a.v) + static_cast<int64_t>(h) * D + vcol;
-    const T* ksrc = static_cast<const T*>(a.k) + static_cast<int64_t>(h) * D;
-    uint4 v[kPasses];  // all of V's loads, then K's, then the work
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int t = min(vrow + i * kRows, n - 1);
-      v[i] = *reinterpret_cast<const uint4*>(vsrc + (it.row + t) * a.v_stride);
-    }
-    if (l.u < l.units) {
+    if (mine) {
       for (int t = l.r0; t < n; t += l.step) {
-        const int slot = it.lo + t;
-        Raw<T> raw;
         Turn turn;
-        load_raw<T>(raw, ksrc + (it.row + t) * a.k_stride, l.u, a.rot, a.interleaved);
+        const int slot = it.lo + t;
+        if (t != l.r0) load_raw<T>(raw, ksrc + t * a.k_stride + h * D, l.u, a.rot, a.interleaved);
         if (a.rot) load_turn(turn, rotation_row(a, it.pos + slot), l.u, a.rot, a.interleaved);
         rotate_unit<T>(raw, turn, kp + slot * D, tile + slot * D, l.u, a.rot, a.interleaved);
       }
@@ -325,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(AppendArgs a) 
       const int t = vrow + i * kRows;
       if (t < n) *reinterpret_cast<uint4*>(vp + (it.lo + t) * D + vcol) = v[i];
     }
+    if (h + 1 < h1) load(h + 1);  // in flight during this head's metadata
     if (a.box == nullptr) continue;
     for (int i = threadIdx.x; i < it.lo * kChunks; i += kThreads)
       *reinterpret_cast<uint4*>(tile + i * kChunk) = *reinterpret_cast<const uint4*>(kp + i * kChunk);
@@ -346,20 +374,13 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(AppendArgs a) 
   }
 }
 
-// Whether x, off by at most e, may round to two different bf16 numbers.
-__device__ __forceinline__ bool near_bf16_border(float x, float e) {
-  const uint32_t b = __float_as_uint(x);
-  const float ulp = __uint_as_float(max(b & 0x7f800000u, 24u << 23) - (23u << 23));
-  return fabsf(static_cast<float>(static_cast<int>(b & 0xffffu) - 0x8000)) * ulp <= e;
-}
-
 // One row of D numbers, D/32 of them per lane, to codes: the lane's codes come
 // back packed, the pair (step, zero) on every lane.  x: the numbers in fp32,
 // each off by at most err (one bound for the row); exact(e) gives number e in
-// 64 bits.  Nearly every row is decided in fp32: only where the extremes are
-// near a border between two bf16 numbers, or a quotient near one between two
-// codes, are the exact numbers asked (1 row and 1 number in some ten thousand).
-// All in 64 bits cost 1500 issue slots per token and KV head, 4 times as many.
+// 64 bits.  Nearly every row is decided in fp32: only where step or zero may
+// round to two bf16 numbers, or a quotient is near a border between two codes,
+// are the exact numbers asked (rotated keys: 1 row and 1 number in some ten
+// thousand).  All in 64 bits cost four times the issue slots.
 template <int E, class F>
 __device__ __forceinline__ uint32_t quantise_row(const float (&x)[E], float err, F exact, uint32_t* step_zero) {
   float mn = x[0], mx = x[0];
@@ -370,10 +391,15 @@ __device__ __forceinline__ uint32_t quantise_row(const float (&x)[E], float err,
   }
   asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(mn) : "f"(mn));
   asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mx) : "f"(mx));
-  float step = (mx - mn) * (1.0f / 15.0f), zero = mn;
-  // step: 2·err of the extremes, and three roundings of fp32
-  if (near_bf16_border(step, err * 0.14f + fabsf(step) * 0x1p-22f) || (err > 0.f && near_bf16_border(mn, err)) ||
-      !(mx - mn <= 3e38f)) {
+  auto pair = [](float a, float b) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  };
+  // step: off by 2·err/15 of the extremes, and three roundings of fp32
+  float step = (mx - mn) * (1.0f / 15.0f);
+  const float es = err * 0.14f + step * 0x1p-22f;
+  uint32_t sw = pair(step - es, step + es), zw = pair(mn - err, mn + err);
+  if (sw != __byte_perm(sw, 0, 0x1010) || zw != __byte_perm(zw, 0, 0x1010) || !(step <= 3e38f)) {
     double dmn = exact(0), dmx = dmn;
 #pragma unroll
     for (int e = 1; e < E; ++e) {
@@ -385,27 +411,33 @@ __device__ __forceinline__ uint32_t quantise_row(const float (&x)[E], float err,
       dmn = fmin(dmn, __shfl_xor_sync(0xffffffffu, dmn, o));
       dmx = fmax(dmx, __shfl_xor_sync(0xffffffffu, dmx, o));
     }
-    step = __double2float_rn((dmx - dmn) / 15.0);
-    zero = __double2float_rn(dmn);
+    sw = pair(__double2float_rn((dmx - dmn) / 15.0), 0.f);
+    zw = pair(__double2float_rn(dmn), 0.f);
   }
-  bf16 sb = __float2bfloat16_rn(step);
-  if (!(__bfloat162float(sb) >= 1e-30f)) sb = __ushort_as_bfloat16(0);
-  const bf16 zb = __float2bfloat16_rn(zero);
-  step = __bfloat162float(sb);
-  zero = __bfloat162float(zb);
-  const float inv = step > 0.f ? 1.0f / step : 0.f;
+  step = bf16_lo(sw);
+  const float zero = bf16_lo(zw);
+  if (!(step >= 1e-30f)) step = 0.f;
+  const float inv = step > 0.f ? 1.0f / step : 0.f, off = -zero * inv;
+  // codes: f is off by err·inv and by the roundings of inv, off and the sum,
+  // 2⁻²⁴·(3·|off| + 48) at most; adding 1.5·2²³ rounds it to a whole number in
+  // the low bits
   uint32_t codes = 0;
+  float worst = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const float f = (x[e] - zero) * inv;
-    float n = rintf(f);
-    // f is off by err·inv, three roundings of at most 16·2⁻²⁴, and the rounding of x − zero
-    if (fabsf(f - n) > 0.5f - 4e-6f - err * inv && step > 0.f)
-      n = __double2float_rn(rint((exact(e) - static_cast<double>(zero)) / static_cast<double>(step)));
-    codes |= static_cast<uint32_t>(fminf(fmaxf(n, 0.f), 15.f)) << (4 * e);
+    const float f = fminf(fmaxf(fmaf(x[e], inv, off), 0.f), 15.f), t = f + 12582912.f;
+    worst = fmaxf(worst, fabsf(f - (t - 12582912.f)));
+    codes += (__float_as_uint(t) - 0x4b400000u) << (4 * e);
   }
-  *step_zero = static_cast<uint32_t>(__bfloat16_as_ushort(sb)) |
-               (static_cast<uint32_t>(__bfloat16_as_ushort(zb)) << 16);
+  if (!(worst <= 0.5f - 4e-6f - fabsf(off) * 2e-7f - err * inv) && step > 0.f) {
+    codes = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const double n = rint((exact(e) - static_cast<double>(zero)) / static_cast<double>(step));
+      codes |= static_cast<uint32_t>(fmin(fmax(n, 0.0), 15.0)) << (4 * e);
+    }
+  }
+  *step_zero = (__float_as_uint(step) >> 16) | (__float_as_uint(zero) & 0xffff0000u);
   return codes;
 }
 
@@ -448,43 +480,46 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_q4_kernel(AppendArgs 
   const bool turns = j < a.rot, low = a.interleaved || j < half;
   const int other = !turns || a.interleaved ? j : (low ? j + half : j - half);
   const int angle = a.interleaved ? j / 2 : (low ? j : j - half);
+  struct Numbers {
+    float x[E], z[E], v[E], c[E], s[E];
+  };
+  auto load = [&](Numbers& m, int h, int t) {
+    const T* ksrc = static_cast<const T*>(a.k) + (it.row + t) * a.k_stride + h * D;
+    load_lane<T, E>(ksrc + j, m.x);
+    load_lane<T, E>(ksrc + other, m.z);
+    load_lane<T, E>(static_cast<const T*>(a.v) + (it.row + t) * a.v_stride + h * D + j, m.v);
+    if (turns) {
+      const float* cs = rotation_row(a, it.pos + it.lo + t);
+      if (a.interleaved) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          m.c[e] = m.c[e + 1] = cs[angle + e / 2];
+          m.s[e] = m.s[e + 1] = cs[half + angle + e / 2];
+        }
+      } else {
+        load_lane<float, E>(cs + angle, m.c);
+        load_lane<float, E>(cs + half + angle, m.s);
+      }
+    }
+  };
+  Numbers next;
+  if (warp < n) load(next, h0, warp);
   for (int h = h0; h < h1; ++h) {
     unsigned char* page = static_cast<unsigned char*>(a.k_pool) +
                           (static_cast<size_t>(it.phys) * a.Hkv + h) * (S / kTile) * R;
-    const T* ksrc = static_cast<const T*>(a.k) + static_cast<int64_t>(h) * D;
-    const T* vsrc = static_cast<const T*>(a.v) + static_cast<int64_t>(h) * D;
     for (int t = warp; t < n; t += kWarps) {
       const int slot = it.lo + t;
       float x[E], z[E], v[E], c[E], s[E];
-      load_lane<T, E>(ksrc + (it.row + t) * a.k_stride + j, x);
-      load_lane<T, E>(ksrc + (it.row + t) * a.k_stride + other, z);
-      load_lane<T, E>(vsrc + (it.row + t) * a.v_stride + j, v);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        c[e] = 1.f;
-        s[e] = 0.f;
+        x[e] = next.x[e];
+        v[e] = next.v[e];
+        z[e] = a.interleaved ? next.z[e ^ 1] : next.z[e];  // the pair's other number
+        c[e] = turns ? next.c[e] : 1.f;
+        s[e] = turns ? next.s[e] : 0.f;
       }
-      if (turns) {
-        const float* cs = rotation_row(a, it.pos + slot);
-        if (a.interleaved) {
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            c[e] = c[e + 1] = cs[angle + e / 2];
-            s[e] = s[e + 1] = cs[half + angle + e / 2];
-          }
-        } else {
-          load_lane<float, E>(cs + angle, c);
-          load_lane<float, E>(cs + half + angle, s);
-        }
-      }
-      if (a.interleaved) {  // the pair's other number
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float keep = z[e];
-          z[e] = z[e + 1];
-          z[e + 1] = keep;
-        }
-      }
+      if (t + kWarps < n) load(next, h, t + kWarps);  // in flight during this token's work
+      else if (h + 1 < h1) load(next, h + 1, warp);
       // number e: x·c − z·s for the first of a pair, x·c + z·s for the second
 #pragma unroll
       for (int e = 0; e < E; ++e)
@@ -609,12 +644,15 @@ int item_count(const int32_t* indptr, int rows, int batch, int S) {
   return indptr == nullptr ? batch : rows / S + 2 * batch;
 }
 
-// KV heads per CTA: one while that gives the GPU at most four waves of five CTAs
-// per SM (a decode step, a short chunk: latency), else as many as keep four
-// (prompts: the page lookups cost 15 of 100 us with one head per CTA).
-int heads_per_cta(int items, int Hkv) {
-  const int64_t waves4 = 20ll * sm_count();
-  const int64_t h = static_cast<int64_t>(items) * Hkv / (waves4 > 0 ? waves4 : 1);
+// KV heads per CTA: one while items × heads are within the given waves of five
+// CTAs per SM (a decode step, a short chunk: latency), else as many as keep to
+// them (long prompts: the page lookups, metadata tails and launches of ten times
+// as many CTAs cost more than the waves' ends).  Measured on 15k new tokens of 8
+// KV heads: two waves 75.7 us, four 79.6, one head per CTA 84; read-back of 100k
+// tokens of 4-bit cache: four waves 96.9 us, two 97.1, but 4k tokens 15.3 and 17.7.
+int heads_per_cta(int items, int Hkv, int waves) {
+  const int64_t room = 5ll * waves * sm_count();
+  const int64_t h = static_cast<int64_t>(items) * Hkv / (room > 0 ? room : 1);
   return static_cast<int>(h < 1 ? 1 : (h > Hkv ? Hkv : h));
 }
 
@@ -627,7 +665,7 @@ cudaError_t run_append(bool q4, int S, dim3 grid, cudaStream_t st, const AppendA
 
 cudaError_t run_append(bool q4, int dtype, int d, const ekv_new_tokens& n, AppendArgs& a, cudaStream_t st) {
   const int items = item_count(n.indptr, n.num_tokens, a.batch, a.S);
-  a.heads = heads_per_cta(items, a.Hkv);
+  a.heads = heads_per_cta(items, a.Hkv, 2);
   const int per = (a.Hkv + a.heads - 1) / a.heads;
   const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(per * (n.q != nullptr ? 2 : 1)));
   if (dtype == EKV_BF16) return d == 128 ? run_append<bf16, 128>(q4, a.S, grid, st, a) : run_append<bf16, 64>(q4, a.S, grid, st, a);
@@ -690,7 +728,7 @@ cudaError_t launch_q4_read(const ekv_cache_q4& c, const ekv_seqs& s, const int32
              k_out,        v_out,          s.batch,     num_tokens,
              c.num_kv_heads, c.page_size,  c.num_phys_pages, s.max_pages, 1};
   const int items = item_count(indptr, num_tokens, s.batch, c.page_size);
-  a.heads = heads_per_cta(items, c.num_kv_heads);
+  a.heads = heads_per_cta(items, c.num_kv_heads, 4);
   const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>((c.num_kv_heads + a.heads - 1) / a.heads));
   const bool wide = c.head_dim == 128;
   if (out_dtype == EKV_BF16)
