@@ -238,7 +238,8 @@ typedef struct {
   int64_t q_stride;      /* elements from one token's row to the next */
   int64_t k_stride;
   int64_t v_stride;
-  const int32_t* indptr; /* device [batch + 1], nondecreasing; NULL: one token per sequence */
+  const int32_t* indptr; /* device [batch + 1], nondecreasing; NULL: row b is the last token
+                            of sequence b (unused where L_b = 0, an idle slot) */
   int32_t num_tokens;    /* rows of q, k, v and q_out */
   int32_t num_q_heads;   /* Hq (ignored when q is NULL) */
   int32_t dtype;         /* ekv_dtype of q, k, v and q_out */

@@ -187,9 +187,15 @@ ekv_status check_q4(const ekv_cache_q4* c) {
   return aligned16(c->pool) ? EKV_OK : EKV_ERR_INVALID_ARG;
 }
 
+// Positions are counted in 32 bits.
+ekv_status check_positions(const ekv_seqs* s, int page_size) {
+  EKV_TRY(check_seqs(s));
+  return static_cast<int64_t>(s->max_pages) * page_size > INT32_MAX ? EKV_ERR_UNSUPPORTED : EKV_OK;
+}
+
 ekv_status check_rope_append(const ekv_cache& c, const ekv_seqs* seqs, const ekv_rope* rope,
                              const ekv_new_tokens* n) {
-  EKV_TRY(check_seqs(seqs));
+  EKV_TRY(check_positions(seqs, c.page_size));
   if (n == nullptr || n->k == nullptr || n->v == nullptr) return EKV_ERR_INVALID_ARG;
   if (n->dtype != EKV_F32 && n->dtype != EKV_BF16) return EKV_ERR_UNSUPPORTED;
   if ((c.box == nullptr) != (c.mom == nullptr)) return EKV_ERR_INVALID_ARG;
@@ -218,6 +224,7 @@ ekv_status softmax_mod(const ekv_cache& c, const void* pool, const ekv_seqs* seq
                        int32_t T, float scale, const ekv_score_mod* mod, const int32_t* sel, const int32_t* n_sel,
                        int32_t cap, float* out, float* lse, void* ws, size_t ws_bytes, void* stream) {
   EKV_TRY(validate_decode(&c, seqs, q, Hq, scale, 1.5f, sel, n_sel, cap, out));
+  EKV_TRY(check_positions(seqs, c.page_size));
   if (T < 1) return EKV_ERR_INVALID_ARG;
   if (c.dtype != EKV_BF16 || T > kModMaxRows || Hq / c.num_kv_heads * T > kModMaxRows) return EKV_ERR_UNSUPPORTED;
   // rows of the pools are counted in 32 bits
@@ -405,7 +412,7 @@ EKV_API ekv_status ekv_rope_append_q4(const ekv_cache_q4* cache, const ekv_seqs*
 EKV_API ekv_status ekv_q4_read(const ekv_cache_q4* cache, const ekv_seqs* seqs, const int32_t* indptr,
                                int32_t num_tokens, int32_t out_dtype, void* k_out, void* v_out, void* stream) {
   EKV_TRY(check_q4(cache));
-  EKV_TRY(check_seqs(seqs));
+  EKV_TRY(check_positions(seqs, cache->page_size));
   if (out_dtype != EKV_F32 && out_dtype != EKV_BF16) return EKV_ERR_UNSUPPORTED;
   if (cache->num_kv_heads > 65535 || seqs->batch > (1 << 28)) return EKV_ERR_UNSUPPORTED;
   if (indptr == nullptr || num_tokens < 1 || (k_out == nullptr && v_out == nullptr)) return EKV_ERR_INVALID_ARG;

@@ -131,7 +131,7 @@ __device__ __forceinline__ Visible visible_tiles(const ModArgs& a, int b) {
   v.a0 = v.nA = v.b0 = v.n = 0;
   if (v.start >= L) return v;
   int lo = v.start;
-  if (a.window > 0) lo = max(lo, L - a.T - a.window + 1);
+  if (a.window > 0 && a.window < L) lo = max(lo, L - a.T - a.window + 1);  // a longer one hides nothing
   const int t_end = (L + kTile - 1) / kTile;
   v.b0 = lo / kTile;
   if (v.prefix > v.start && lo > v.start) {
@@ -1393,8 +1393,9 @@ cudaError_t launch_softmax_mod(const ekv_cache& c, const void* pool, const ekv_s
     a.prefix_lens = mod->prefix_lens;
     a.starts = mod->starts;
     a.window = mod->window;
-    if (mod->softcap > 0.f) {
-      a.capx = scale / mod->softcap;
+    // a cap of 1e30 changes no score in fp32; under 1e-30 scores are ±cap or 0
+    if (mod->softcap > 0.f && mod->softcap < 1e30f) {
+      a.capx = scale / fmaxf(mod->softcap, 1e-30f);
       a.cap2 = mod->softcap * kLog2e;
     }
   }

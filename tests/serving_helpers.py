@@ -123,6 +123,7 @@ class Paged:
 
 def sees(i, j, L, start, prefix, window):
     j = np.asarray(j)
+    j = j.astype(np.int64)
     ok = (j < prefix) | ((j <= i) & ((window == 0) | (i - j < window)))
     return ok & (j >= start) & (j < L) & (i >= 0)
 
@@ -151,8 +152,9 @@ def decode64(pg, K, V, q, scale, *, cap=0.0, slopes=None, window=0, prefix=None,
                 z = Kb[m] @ q[b, t, hq] * scale
                 size = (np.abs(Kb[m]) @ np.abs(q[b, t, hq]) * scale).max()
                 s = cap * np.tanh(z / cap) if cap else z
+                top_cap = min(cap, np.abs(z).max())  # a score is no larger than either
                 dist = np.abs(i - j[m])
-                e = d * 2.0 ** -23 * size + 4 * 2.0 ** -23 * (cap + np.abs(z).max() + 8)
+                e = d * 2.0 ** -23 * size + 4 * 2.0 ** -23 * (top_cap + np.abs(z).max() + 8)
                 if slopes is not None:
                     s = s - slopes[hq] * dist
                     e += 4 * 2.0 ** -23 * 150 * abs(slopes[hq])  # what lies further off in score weighs nothing

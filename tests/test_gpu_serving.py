@@ -118,6 +118,27 @@ def test_rope_append_without_rotation_matches_append_and_rotates_in_place():
     assert B.ekv_get_error() == 0
 
 
+def test_appends_without_metadata():
+    """box and mom left out: the same K, V and q, and nothing else is touched."""
+    pg = Paged([50, 16, 129], 2, 64, 32, seed=7)
+    new = [50, 3, 129]
+    q, k, v, q_out, indptr = _tokens(pg, new, 4, BF, True, 0)
+    seqs, rope = B.make_seqs(pg.table, pg.seq_lens), B.make_rope(rope_table(129, 64))
+    got = []
+    for meta in (True, False):
+        kp, vp = pg.pools()[0].fill_(1), pg.pools()[0].fill_(2)
+        c = B.make_cache(kp, vp)
+        if not meta:
+            c.box = c.mom = None
+        B.ekv_rope_append(c, seqs, rope, B.make_new_tokens(k, v, q, q_out, indptr))
+        pool = torch.zeros_like(pg.pool_q4())
+        box = torch.zeros(2, pg.n_phys, 2, 64, dtype=BF, device="cuda")
+        B.ekv_rope_append_q4(B.make_cache_q4(pool, 64, *((box, box.clone()) if meta else ())), seqs, rope,
+                             B.make_new_tokens(k, v, q, q_out, indptr))
+        got.append((kp, vp, pool, q_out.clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and B.ekv_get_error() == 0
+
+
 def test_append_faults_are_flagged_and_skipped():
     pg = Paged([40, 33, 20], 2, 64, 16, seed=6)
     rope = B.make_rope(rope_table(35, 64))
@@ -295,6 +316,10 @@ DECODES = {
     "window": ([600, 40, 100, 5], 2, 4, 128, 16, 1, {"window": 37}),
     "window_one": ([600, 1], 2, 2, 128, 16, 1, {"window": 1}),
     "window_wide": ([600, 40], 2, 2, 64, 32, 1, {"window": 10 ** 9}),
+    "window_widest": ([600, 40, 1], 2, 2, 64, 16, 5, {"window": 2 ** 31 - 1, "prefix": [2 ** 31 - 1, 3, -2 ** 31],
+                                                      "start": [-2 ** 31, 2, 0]}),
+    "cap_widest": ([200], 1, 2, 64, 16, 1, {"cap": 3e38}),
+    "cap_smallest": ([200], 1, 2, 64, 16, 1, {"cap": 1e-37}),
     "prefix": ([600, 40, 100, 5], 2, 4, 128, 16, 1, {"window": 20, "prefix": [33, 39, 100, 7]}),
     "prefix_near": ([600, 40], 1, 4, 128, 16, 1, {"window": 32, "prefix": [566, 5]}),
     "start": ([600, 40, 100, 5], 2, 4, 128, 16, 1, {"start": [599, 16, 0, 2]}),

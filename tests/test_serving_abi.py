@@ -58,6 +58,7 @@ def _append(cache=None, seqs=None, rope=None, new=None):
 
 APPEND_REFUSALS = [
     (dict(seqs=_seqs(batch=0)), INVALID), (dict(seqs=_seqs(page_table=None)), INVALID),
+    (dict(seqs=_seqs(max_pages=2 ** 27)), UNSUPPORTED),                        # positions past 2³¹
     (dict(rope=_rope(cos_sin=None)), INVALID), (dict(rope=_rope(cos_sin=FAKE + 4)), INVALID),
     (dict(rope=_rope(max_pos=0)), INVALID), (dict(rope=_rope(rot_dim=0)), INVALID),
     (dict(rope=_rope(rot_dim=24)), INVALID), (dict(rope=_rope(rot_dim=144)), INVALID),
@@ -103,7 +104,7 @@ def test_read_refuses():
     assert _read(indptr=None) == INVALID and _read(n=0) == INVALID
     assert _read(k=None, v=None) == INVALID and _read(k=FAKE + 4) == INVALID
     assert _read(dtype=3) == UNSUPPORTED and _read(cache=_q4(page_size=64)) == UNSUPPORTED
-    assert _read(seqs=_seqs(max_pages=0)) == INVALID
+    assert _read(seqs=_seqs(max_pages=0)) == INVALID and _read(seqs=_seqs(max_pages=2 ** 27)) == UNSUPPORTED
     assert B.lib().ekv_q4_read(None, by(_seqs()), FAKE, 4, 0, FAKE, FAKE, None) == INVALID
 
 
@@ -123,7 +124,7 @@ DECODE_REFUSALS = [
     (dict(mod=_mod(softcap=-1.0)), INVALID), (dict(mod=_mod(softcap=float("inf"))), INVALID),
     (dict(mod=_mod(softcap=float("nan"))), INVALID), (dict(mod=_mod(window=-1)), INVALID),
     (dict(sel=FAKE), INVALID), (dict(n_sel=FAKE), INVALID), (dict(cap=4), INVALID), (dict(cap=0), INVALID),
-    (dict(seqs=_seqs(batch=-1)), INVALID),
+    (dict(seqs=_seqs(batch=-1)), INVALID), (dict(seqs=_seqs(max_pages=2 ** 27), cap=2 ** 27), UNSUPPORTED),
     (dict(ws=None), WORKSPACE), (dict(ws=0x100010), WORKSPACE), (dict(ws_bytes=1000), WORKSPACE),
 ]
 
