@@ -338,6 +338,10 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(AppendArgs a) 
     const size_t ph = static_cast<size_t>(it.phys) * a.Hkv + h;
     T* kp = static_cast<T*>(a.k_pool) + ph * S * D;
     T* vp = static_cast<T*>(a.v_pool) + ph * S * D;
+    // the page's earlier keys, for its metadata: on their way with the new ones
+    if (a.box != nullptr)
+      for (int i = threadIdx.x; i < it.lo * kChunks; i += kThreads)
+        *reinterpret_cast<uint4*>(tile + i * kChunk) = *reinterpret_cast<const uint4*>(kp + i * kChunk);
     if (mine) {
       for (int t = l.r0; t < n; t += l.step) {
         Turn turn;
@@ -354,8 +358,6 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(AppendArgs a) 
     }
     if (h + 1 < h1) load(h + 1);  // in flight during this head's metadata
     if (a.box == nullptr) continue;
-    for (int i = threadIdx.x; i < it.lo * kChunks; i += kThreads)
-      *reinterpret_cast<uint4*>(tile + i * kChunk) = *reinterpret_cast<const uint4*>(kp + i * kChunk);
     __syncthreads();
     const int j = threadIdx.x;
     if (j < D) {
@@ -430,11 +432,16 @@ __device__ __forceinline__ uint32_t quantise_row(const float (&x)[E], float err,
     codes += (__float_as_uint(t) - 0x4b400000u) << (4 * e);
   }
   if (!(worst <= 0.5f - 4e-6f - fabsf(off) * 2e-7f - err * inv) && step > 0.f) {
+    // the code below (a quotient that slips past a whole number changes nothing),
+    // and the exact border above it: (n + ½)·step has 13 bits
     codes = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const double n = rint((exact(e) - static_cast<double>(zero)) / static_cast<double>(step));
-      codes |= static_cast<uint32_t>(fmin(fmax(n, 0.0), 15.0)) << (4 * e);
+      const double d = exact(e) - static_cast<double>(zero);
+      const float n = floorf(fminf(fmaxf(__double2float_rn(d * static_cast<double>(inv)), 0.f), 15.f));
+      const double border = static_cast<double>((n + 0.5f) * step);
+      const int k = static_cast<int>(n);
+      codes |= static_cast<uint32_t>(min(15, k + (d > border || (d == border && (k & 1)) ? 1 : 0))) << (4 * e);
     }
   }
   *step_zero = (__float_as_uint(step) >> 16) | (__float_as_uint(zero) & 0xffff0000u);
@@ -507,6 +514,16 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_q4_kernel(AppendArgs 
   for (int h = h0; h < h1; ++h) {
     unsigned char* page = static_cast<unsigned char*>(a.k_pool) +
                           (static_cast<size_t>(it.phys) * a.Hkv + h) * (S / kTile) * R;
+    // the page's earlier codes, for its metadata: on their way with the new tokens
+    if (a.box != nullptr) {
+      for (int i = threadIdx.x; i < it.lo * (kRow / 4); i += kThreads) {
+        const int slot = i / (kRow / 4), cc = i - slot * (kRow / 4);
+        reinterpret_cast<uint32_t*>(codes_s)[i] =
+            reinterpret_cast<const uint32_t*>(page + (slot / kTile) * R + (slot % kTile) * kRow)[cc];
+      }
+      for (int slot = threadIdx.x; slot < it.lo; slot += kThreads)
+        sz_s[slot] = reinterpret_cast<const uint32_t*>(page + (slot / kTile) * R + 16 * D)[slot % kTile];
+    }
     for (int t = warp; t < n; t += kWarps) {
       const int slot = it.lo + t;
       float x[E], z[E], v[E], c[E], s[E];
@@ -558,13 +575,6 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_q4_kernel(AppendArgs 
       }
     }
     if (a.box == nullptr) continue;
-    for (int i = threadIdx.x; i < it.lo * (kRow / 4); i += kThreads) {
-      const int slot = i / (kRow / 4), cc = i - slot * (kRow / 4);
-      reinterpret_cast<uint32_t*>(codes_s)[i] =
-          reinterpret_cast<const uint32_t*>(page + (slot / kTile) * R + (slot % kTile) * kRow)[cc];
-    }
-    for (int slot = threadIdx.x; slot < it.lo; slot += kThreads)
-      sz_s[slot] = reinterpret_cast<const uint32_t*>(page + (slot / kTile) * R + 16 * D)[slot % kTile];
     __syncthreads();
     const int col = threadIdx.x;
     if (col < D) {

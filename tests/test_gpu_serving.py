@@ -246,8 +246,8 @@ def test_rope_append_q4(name, dtype):
 def test_q4_rows_of_one_value_borders_and_one_output():
     """Constant rows, rows whose quotients fall on borders between codes, tiny and large scales."""
     d = 64
-    pg = Paged([8], 1, d, 16, seed=9)
-    x = np.zeros((8, d), np.float64)
+    pg = Paged([12], 1, d, 16, seed=9)
+    x = np.zeros((12, d), np.float64)
     x[0] = 1.5                                        # one value: step 0
     x[1] = np.arange(d) % 31 / 2.0                    # step 1, halves everywhere
     x[2] = -x[1] * 2.0 ** 60
@@ -256,23 +256,28 @@ def test_q4_rows_of_one_value_borders_and_one_output():
     x[5, 0] = 300.0                                   # one outlier
     x[6] = 1000 + np.arange(d) % 8
     x[7] = (np.arange(d) - 31) / 4.0
+    x[8] = 2.0 ** 20 + np.arange(d) % 13 / 8.0        # a step far below zero's own spacing
+    x[9] = -(2.0 ** 23) + np.arange(d) % 2
+    x[10] = np.arange(d) % 16 + (np.arange(d) % 3 - 1) * 2.0 ** -20   # next to the codes
+    x[11] = np.arange(d) % 15 + 0.5 + (np.arange(d) % 3 - 1) * 2.0 ** -19   # next to the borders
+    x[11, :2] = 0, 15
     v = torch.tensor(x, dtype=F32, device="cuda")[:, None]
     assert np.array_equal(np64(v)[:, 0], x)
     pool = pg.pool_q4()
     cache = B.make_cache_q4(pool, d)
     seqs = B.make_seqs(pg.table, pg.seq_lens)
-    indptr = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    indptr = torch.tensor([0, 12], dtype=torch.int32, device="cuda")
     B.ekv_rope_append_q4(cache, seqs, None, B.make_new_tokens(v, v, indptr=indptr))
     codes, step, zero = unpack(pool, d)
     ph = int(pg.table_h[0, 0])
-    for r in range(8):
+    for r in range(12):
         c, st, ze = quantise64(x[r])
         for part in (0, 1):
             assert np.array_equal(codes[ph, 0, 0, part, r], c), r
             assert step[ph, 0, 0, part, r] == st and zero[ph, 0, 0, part, r] == ze
-    only = torch.zeros(8, 1, d, device="cuda")
+    only = torch.zeros(12, 1, d, device="cuda")
     B.ekv_q4_read(cache, seqs, indptr, None, only)
-    assert torch.equal(only.cpu()[:, 0].double(), torch.tensor(q4_values(pool, d)[1][ph, 0, :8].astype(np.float32)).double())
+    assert torch.equal(only.cpu()[:, 0].double(), torch.tensor(q4_values(pool, d)[1][ph, 0, :12].astype(np.float32)).double())
     assert B.ekv_get_error() == 0
 
 
