@@ -267,6 +267,11 @@ __device__ void rotate_queries(const AppendArgs& a, const PageItem& it, int h0, 
   }
 }
 
+#define EKV_R4(n) 1.0 / (n), 1.0 / ((n) + 1), 1.0 / ((n) + 2), 1.0 / ((n) + 3)
+__constant__ double kReciprocal[33] = {0.0, EKV_R4(1), EKV_R4(5), EKV_R4(9), EKV_R4(13), EKV_R4(17), EKV_R4(21),
+                                       EKV_R4(25), EKV_R4(29)};
+#undef EKV_R4
+
 // Metadata of one coordinate over tokens 0..n−1 of a page, as meta.cu computes
 // it: exact extremes, mean and population variance in float64 in token order
 // with one rounding per operation.  P: 16 or 32, at least n; value(t) is called
@@ -286,10 +291,16 @@ __device__ __forceinline__ void column_meta(F value, int n, float* mx, float* mn
       s = __dadd_rn(s, static_cast<double>(x[t]));
     }
   }
-  // a full page's n is a power of two: its quotients are products, bit for bit,
-  // without the division's long chain
-  const double dn = static_cast<double>(n), by = 1.0 / P;
-  const double m = n == P ? __dmul_rn(s, by) : __ddiv_rn(s, dn);
+  // s/n correctly rounded by Markstein's theorem (IBM J. Res. Dev. 34, 1990): with
+  // y = 1/n correctly rounded and q = s·y, the rest r = s − q·n is exact and
+  // q + r·y rounds to the quotient.  A table of y in place of the division's
+  // chain of dependent steps.
+  const double dn = static_cast<double>(n), y = kReciprocal[n];
+  auto over_n = [&](double a) {
+    const double q = __dmul_rn(a, y), r = __fma_rn(-q, dn, a), c = __fma_rn(r, y, q);
+    return fabs(a) <= 1.7976931348623157e308 ? c : q;  // infinities and NaN: as they are
+  };
+  const double m = over_n(s);
 #pragma unroll
   for (int t = 0; t < P; ++t) {
     if (t < n) {
@@ -300,7 +311,7 @@ __device__ __forceinline__ void column_meta(F value, int n, float* mx, float* mn
   *mx = hi;
   *mn = lo;
   *mean = m;
-  *var = n == P ? __dmul_rn(v, by) : __ddiv_rn(v, dn);
+  *var = over_n(v);
 }
 
 // grid: (items, CTAs for K and V, then as many for the queries); a CTA takes

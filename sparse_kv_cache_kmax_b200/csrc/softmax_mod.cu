@@ -176,15 +176,15 @@ struct Tile {
 __device__ __forceinline__ Tile resolve_tile(const ModArgs& a, const Segment& s, int t) {
   Tile r{-1, -kTile};
   if (t < s.t0 || s.vis.n == 0) return r;
-  const int tpp = a.S / kTile;
+  const int sh = a.S == kTile ? 0 : 1, tpp = 1 << sh;  // tiles of a page: 1 or 2
   int lp, part;
   if (a.sel == nullptr) {
     const int tile = t < s.vis.nA ? s.vis.a0 + t : s.vis.b0 + t - s.vis.nA;
-    lp = tile / tpp;
-    part = tile - lp * tpp;
+    lp = tile >> sh;
+    part = tile & (tpp - 1);
   } else {
-    const int slot = t / tpp;
-    part = t - slot * tpp;
+    const int slot = t >> sh;
+    part = t & (tpp - 1);
     if (slot >= max(0, min(a.n_sel[s.unit], a.cap))) return r;  // the empty unit's tile
     lp = a.sel[static_cast<size_t>(s.unit) * a.cap + slot];
     if (lp < 0 || lp >= (s.vis.L + a.S - 1) / a.S) {
@@ -211,13 +211,13 @@ __device__ __forceinline__ Tile resolve_tile(const ModArgs& a, const Segment& s,
 
 // Position of a segment's first (last) tile, whether or not it can be read.
 __device__ __forceinline__ int tile_position(const ModArgs& a, const Segment& s, int t) {
-  const int tpp = a.S / kTile;
+  const int sh = a.S == kTile ? 0 : 1;
   if (s.vis.n == 0) return 0;
   if (a.sel == nullptr) return (t < s.vis.nA ? s.vis.a0 + t : s.vis.b0 + t - s.vis.nA) * kTile;
-  const int slot = t / tpp;
+  const int slot = t >> sh;
   if (slot >= max(0, min(a.n_sel[s.unit], a.cap))) return 0;
   const int lp = a.sel[static_cast<size_t>(s.unit) * a.cap + slot];
-  return lp < 0 || lp >= a.max_pages ? 0 : lp * a.S + (t - slot * tpp) * kTile;
+  return lp < 0 || lp >= a.max_pages ? 0 : lp * a.S + (t - (slot << sh)) * kTile;
 }
 
 // The distance that the bias of a piece is measured from, so that far tokens
@@ -329,19 +329,19 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   per = max(per, a.min_tiles);
   bool aligned = false;
   if (static_cast<long long>(groups) * mult <= ctas) {
-    auto pieces = [&](int by) {
+    auto fits = [&](int by) {
       const float inv = 1.f / static_cast<float>(by);
-      return sum_over_groups([inv](int n) { return n > 0 ? piece_count(n, inv) : 0; });
+      return sum_over_groups([inv](int n) { return n > 0 ? piece_count(n, inv) : 0; }) <= ctas;
     };
-    aligned = pieces(per) <= ctas;
-    if (!aligned) {
-      // equal units: what the CTAs of one would take
-      const uint32_t units = static_cast<uint32_t>(groups * mult), each = ctas / units;
-      const int by = static_cast<int>((static_cast<uint32_t>(total / units) + each - 1) / each);
-      if (by >= per && by - per <= a.slack_tiles && pieces(by) <= ctas) {
-        aligned = true;
-        per = by;
-      }
+    // what the CTAs of one of equal units would take; else the equal run
+    const float units = static_cast<float>(groups * mult);
+    const float each = floorf(static_cast<float>(ctas) / units + 1e-3f);
+    const int by = max(a.min_tiles, static_cast<int>(ceilf(static_cast<float>(total) / (units * each))));
+    if (by - per <= a.slack_tiles && fits(by)) {
+      aligned = true;
+      per = by;
+    } else {
+      aligned = by != per && fits(per);
     }
   }
   if (tid == 0) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
