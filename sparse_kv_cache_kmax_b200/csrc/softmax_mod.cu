@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   unsigned char* ring = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   float* red = reinterpret_cast<float*>(ring + NS * ST * Sh::slot_bytes);
   if (tid < NS * ST) {
-    mbar_init(&bars[tid], 1);
+    mbar_init(&bars[tid], U);  // an arrival per tile
     fence_mbar_init();
   }
   if (!Q4 && tid == 0) {
@@ -425,27 +425,25 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
 
   unsigned char* my_ring = ring + stream * ST * Sh::slot_bytes;
   uint64_t* my_bar = bars + stream * ST;
-  int it = 0;  // steps this stream has consumed: ring position and parity
+  int ring_at = 0;            // the slot whose turn it is
+  unsigned int parity = 0;    // and its barrier's phase
   Tile cur, nxt;
-  auto issue = [&](const int (&at)[U], int n) {  // lane 0 of the stream's first warp: a step into ring position n
-    const int sl = n % ST;
-    unsigned char* dst = my_ring + sl * Sh::slot_bytes;
-    int tiles = 0;
+  // One tile into its place of slot sl, by the lane that looked it up: a step's
+  // copies start side by side, and no lane has to be told another's tile.
+  auto issue = [&](const Tile& x, int sl, int u) {
+    if (x.at < 0) {
+      mbar_arrive(&my_bar[sl]);
+      return;
+    }
+    unsigned char* dst = my_ring + sl * Sh::slot_bytes + u * (Sh::slot_bytes / U);
+    mbar_arrive_expect_tx(&my_bar[sl], Sh::tile_bytes);
+    if constexpr (Q4) {
+      bulk_g2s(dst, a.pool + static_cast<size_t>(x.at) * Sh::tile_bytes, Sh::tile_bytes, &my_bar[sl]);
+    } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u) tiles += at[u] >= 0 ? 1 : 0;
-    mbar_arrive_expect_tx(&my_bar[sl], static_cast<unsigned int>(tiles * Sh::tile_bytes));
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (at[u] < 0) continue;
-      if constexpr (Q4) {
-        bulk_g2s(dst + u * (Sh::slot_bytes / U), a.pool + static_cast<size_t>(at[u]) * Sh::tile_bytes, Sh::tile_bytes,
-                 &my_bar[sl]);
-      } else {
-#pragma unroll
-        for (int half = 0; half < D / 64; ++half) {
-          tma_2d(dst + half * kTile * 128, &kmap, half * 64, at[u] * kTile, &my_bar[sl]);
-          tma_2d(dst + (D / 64 + half) * kTile * 128, &vmap, half * 64, at[u] * kTile, &my_bar[sl]);
-        }
+      for (int half = 0; half < D / 64; ++half) {
+        tma_2d(dst + half * kTile * 128, &kmap, half * 64, x.at * kTile, &my_bar[sl]);
+        tma_2d(dst + (D / 64 + half) * kTile * 128, &vmap, half * 64, x.at * kTile, &my_bar[sl]);
       }
     }
   };
@@ -461,10 +459,6 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   };
   auto lookup = [&](const Segment& s, int batch) {
     return resolve_tile(a, s, s.t1 - 1 - (U * (stream + NS * (kSteps * batch + lane / U)) + lane % U));
-  };
-  auto pick = [&](int x, int k, int (&to)[U]) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) to[u] = __shfl_sync(0xffffffffu, x, (k % kSteps) * U + u);
   };
   const int rows = a.G * a.T;
   // a lane's share of its query row (row g of each group of 8): bf16 caches, the
@@ -491,12 +485,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
     }
     const int nk = stream_steps(s);
     cur = lookup(s, 0);
-#pragma unroll
-    for (int k = 0; k < ST; ++k) {
-      int at[U];
-      pick(cur.at, k, at);
-      if (lane == 0 && rg == 0 && k < nk) issue(at, it + k);
-    }
+    const int step = lane / U, sl = ring_at + step < ST ? ring_at + step : ring_at + step - ST;
+    if (rg == 0 && step < ST && step < nk) issue(cur, sl, lane % U);
     if (nk > kSteps - ST) nxt = lookup(s, 1);
   };
   auto stream_sync = [&]() {
@@ -609,15 +599,16 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
 
     // ---- the tiles
     const int nk = stream_steps(now);
-    for (int k = 0; k < nk; ++k, ++it) {
-      if (k > 0 && k % kSteps == 0) {
+    for (int k = 0; k < nk; ++k) {
+      const int in = k & (kSteps - 1);  // within the 32 tiles looked up
+      if (k > 0 && in == 0) {
         cur = nxt;
         nxt = lookup(now, k / kSteps + 1);
       }
       int j0[U];
-      pick(cur.j0, k, j0);
-      const int sl = it % ST;
-      const unsigned int parity = static_cast<unsigned int>(it / ST) & 1u;
+#pragma unroll
+      for (int u = 0; u < U; ++u) j0[u] = __shfl_sync(0xffffffffu, cur.j0, in * U + u);
+      const int sl = ring_at;
       if (!mbar_wait(&my_bar[sl], parity)) mbar_wait(&my_bar[sl], parity);
       unsigned char* const buf = my_ring + sl * Sh::slot_bytes;
       int flags = 3;
@@ -1105,12 +1096,13 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
       }
       // the slot is free: the next copies into it
       stream_sync();
-      const int ahead = k + ST;
-      int at[U];
-      pick(ahead / kSteps == k / kSteps ? cur.at : nxt.at, ahead, at);
-      if (lane == 0 && rg == 0 && ahead < nk) {
+      if (rg == 0 && lane / U == ((in + ST) & (kSteps - 1)) && k + ST < nk) {
         fence_proxy_async_shared();  // the slot's reads come before the copies that refill it
-        issue(at, it + ST);
+        issue(in + ST < kSteps ? cur : nxt, sl, lane % U);
+      }
+      if (++ring_at == ST) {
+        ring_at = 0;
+        parity ^= 1u;
       }
     }
 
