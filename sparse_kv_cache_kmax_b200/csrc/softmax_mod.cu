@@ -75,16 +75,17 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// tanh(x): for |x| ≤ 1 the fifth convergent of Lambert's continued fraction,
-// x(945 + 105x² + x⁴)/(945 + 420x² + 15x⁴) (off by x¹¹/9.8e6 at most), above
-// it (e^2x − 1)/(e^2x + 1), where nothing cancels.
+// tanh(x) for |x| ≤ 1: the fifth convergent of Lambert's continued fraction,
+// off by x¹¹/9.8e6 at most.  Scores under their cap lie there.
+__device__ __forceinline__ float tanh_small(float x) {
+  const float x2 = x * x;
+  return __fdividef(x * fmaf(x2, x2 + 105.f, 945.f), fmaf(x2, fmaf(x2, 15.f, 420.f), 945.f));
+}
+// tanh(x) for any x: above 1 (e^2x − 1)/(e^2x + 1), where nothing cancels.
 __device__ __forceinline__ float tanh_f32(float x) {
-  const float ax = fabsf(x), x2 = x * x;
-  const float e = ex2(fminf(ax, 15.f) * (2.f * kLog2e));
-  const float num = ax <= 1.f ? ax * fmaf(x2, x2 + 105.f, 945.f) : e - 1.f;
-  const float den = ax <= 1.f ? fmaf(x2, fmaf(x2, 15.f, 420.f), 945.f) : e + 1.f;
-  const float t = __fdividef(num, den);
-  return x != x ? x : copysignf(t, x);
+  const float ax = fabsf(x), e = ex2(fminf(ax, 15.f) * (2.f * kLog2e));
+  const float t = copysignf(__fdividef(e - 1.f, e + 1.f), x);
+  return ax > 1.f ? t : tanh_small(x);  // NaN: the second
 }
 
 // d = A·B + c on m16n8k16 bf16 (fragments as mma_bf16 in common.cuh).  d and c
@@ -702,12 +703,28 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
         }
       }
       if (a.cap2 != 0.f) {
+        bool large = false;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[u][nt][e] = a.cap2 * tanh_f32(z[u][nt][e]);
+            for (int e = 0; e < 4; ++e) large |= fabsf(z[u][nt][e]) > 1.f;
+        if (__any_sync(0xffffffffu, large)) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) z[u][nt][e] = a.cap2 * tanh_f32(z[u][nt][e]);
+        } else {  // 8 instructions a score in place of 20
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) z[u][nt][e] = a.cap2 * tanh_small(z[u][nt][e]);
+        }
       }
       if (a.slopes) {
         if (flags & 2) {  // behind the query the bias is linear
