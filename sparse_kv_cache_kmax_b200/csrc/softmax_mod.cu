@@ -64,7 +64,8 @@ struct ModArgs {
   float scale2;  // scale·log2(e), the factor of q·k without a cap
   float capx;    // scale/softcap
   float cap2;    // softcap·log2(e); 0: no cap
-  int window, batch, Hkv, Hq, G, T, S, num_phys, max_pages, cap;
+  int window, batch, Hkv, Hq, G, gsh, T, S,  // G = 1 << gsh
+      num_phys, max_pages, cap;
   int min_tiles;    // the smallest run of a CTA: a step of every warp, for 4 bits of half of them
   int slack_tiles;  // how much longer a run may get where no CTA then crosses units: about the time of a crossing
 };
@@ -125,22 +126,27 @@ struct Visible {
   int L, start, prefix, a0, nA, b0, n;
 };
 
-__device__ __forceinline__ Visible visible_tiles(const ModArgs& a, int b) {
+struct Bounds {  // what the call says of one sequence
+  int L, start, prefix;
+};
+__device__ __forceinline__ Bounds load_bounds(const ModArgs& a, int b) {
+  return Bounds{a.seq_lens[b], a.starts ? a.starts[b] : 0, a.prefix_lens ? a.prefix_lens[b] : 0};
+}
+__device__ __forceinline__ Visible visible_tiles(const ModArgs& a, Bounds s) {
   Visible v;
-  int L = a.seq_lens[b];
   const int most = a.max_pages * a.S;
-  if (L < 0 || L > most) {
+  if (s.L < 0 || s.L > most) {
     raise_flag(EKV_EFLAG_BAD_LEN);
-    L = L < 0 ? 0 : most;
+    s.L = s.L < 0 ? 0 : most;
   }
-  v.L = L;
-  v.start = a.starts ? max(0, a.starts[b]) : 0;
-  v.prefix = a.prefix_lens ? max(0, min(a.prefix_lens[b], L)) : 0;
+  v.L = s.L;
+  v.start = max(0, s.start);
+  v.prefix = max(0, min(s.prefix, s.L));
   v.a0 = v.nA = v.b0 = v.n = 0;
-  if (v.start >= L) return v;
+  if (v.start >= v.L) return v;
   int lo = v.start;
-  if (a.window > 0 && a.window < L) lo = max(lo, L - a.T - a.window + 1);  // a longer one hides nothing
-  const int t_end = (L + kTile - 1) / kTile;
+  if (a.window > 0 && a.window < v.L) lo = max(lo, v.L - a.T - a.window + 1);  // a longer one hides nothing
+  const int t_end = (v.L + kTile - 1) / kTile;
   v.b0 = lo / kTile;
   if (v.prefix > v.start && lo > v.start) {
     v.a0 = v.start / kTile;
@@ -154,9 +160,11 @@ __device__ __forceinline__ Visible visible_tiles(const ModArgs& a, int b) {
 // Tiles of one entry of the work list's outer level: a unit when pages are
 // selected, else a sequence's count per KV head.  At least one: a unit that
 // sees nothing gets one empty tile, which writes its rows.
+__device__ __forceinline__ int selected_tiles(const ModArgs& a, int n_sel) {
+  return max(1, max(0, min(n_sel, a.cap)) * (a.S / kTile));
+}
 __device__ __forceinline__ int group_tiles(const ModArgs& a, int grp) {
-  if (a.sel == nullptr) return max(1, visible_tiles(a, grp).n);
-  return max(1, max(0, min(a.n_sel[grp], a.cap)) * (a.S / kTile));
+  return a.sel ? selected_tiles(a, a.n_sel[grp]) : max(1, visible_tiles(a, load_bounds(a, grp)).n);
 }
 
 // Pieces of about 1/inv tiles that a unit of n tiles is cut into: at least one,
@@ -286,6 +294,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   extern __shared__ unsigned char smem_raw[];
   __shared__ uint64_t bars[NS * ST];
   __shared__ float s_m[NW][8 * NT], s_l[NW][8 * NT], s_c[NW][8 * NT];
+  __shared__ float2 s_row[8 * NT * R];  // what a row's sums are multiplied by, and what is added before
   constexpr bool kSharedQ = Q4 && NT == 1;  // one set of query fragments for all warps, to spare registers
   __shared__ uint2 s_q[kSharedQ ? KS : 1][32];
   __shared__ Segment s_seg[2];  // the unit in work, and the next
@@ -309,16 +318,27 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   // every CTA equally busy but lets one cross units, which costs it a second
   // set of queries and a second merge; cutting every unit into equal pieces
   // costs nothing while there are CTAs enough, so that comes first.  Every warp
-  // works it out by itself, four groups per lane at a time: block-wide scans
-  // cost four times as long (2.4 us of a 24 us call).
+  // works it out by itself, four groups per lane at a time, all their loads first
+  // (block-wide scans took 2.4 us of a 24 us call, loads one by one 1.9 of 15).
   const int mult = a.sel ? 1 : a.Hkv, groups = a.sel ? a.batch * a.Hkv : a.batch;
-  int mine[4];  // tiles of groups 4·lane .. + 3 of the chunk in work
+  int mine[4];  // tiles of groups 32·i + lane of the chunk in work
   int held = -1;
   auto load_chunk = [&](int c0) {
     if (held == c0) return;
     held = c0;
+    Bounds s[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mine[i] = c0 + 4 * lane + i < groups ? group_tiles(a, c0 + 4 * lane + i) : 0;
+    for (int i = 0; i < 4; ++i) {
+      if (c0 + 32 * i >= groups) continue;
+      const int grp = min(c0 + 32 * i + lane, groups - 1);
+      if (a.sel) s[i].L = a.n_sel[grp];
+      else s[i] = load_bounds(a, grp);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      mine[i] = c0 + 32 * i + lane >= groups ? 0
+                : a.sel                      ? selected_tiles(a, s[i].L)
+                                             : max(1, visible_tiles(a, s[i]).n);
   };
   auto sum_over_groups = [&](auto value) {  // value(tiles), times the units of a group
     long long total = 0;
@@ -361,44 +381,33 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   int grp = -1, grp_tiles = 0;
   for (int c0 = 0; c0 < groups && grp < 0; c0 += 128) {
     load_chunk(c0);
-    int len[4], x = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      len[i] = (aligned && mine[i] > 0 ? piece_count(mine[i], inv_per) : mine[i]) * mult;
-      x += len[i];
-    }
-    int up = x;  // inclusive scan over the lanes
+      if (grp >= 0 || c0 + 32 * i >= groups) continue;
+      const int len = (aligned && mine[i] > 0 ? piece_count(mine[i], inv_per) : mine[i]) * mult;
+      int up = len;  // inclusive scan over the lanes
 #pragma unroll
-    for (int sh = 1; sh < 32; sh <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, up, sh);
-      if (lane >= sh) up += y;
-    }
-    const int off = start - grp_at < 0x7fffffff ? static_cast<int>(start - grp_at) : 0x7fffffff;
-    int at = up - x, which = -1, tiles = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (which < 0 && at <= off && off < at + len[i]) {
-        which = 4 * lane + i;
-        tiles = mine[i];
-      } else if (which < 0) {
-        at += len[i];
+      for (int sh = 1; sh < 32; sh <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, up, sh);
+        if (lane >= sh) up += y;
       }
-    }
-    const uint32_t hit = __ballot_sync(0xffffffffu, which >= 0);
-    if (hit) {
-      const int from = __ffs(hit) - 1;
-      grp = c0 + __shfl_sync(0xffffffffu, which, from);
-      grp_tiles = __shfl_sync(0xffffffffu, tiles, from);
-      grp_at += __shfl_sync(0xffffffffu, at, from);
-    } else {
-      grp_at += __shfl_sync(0xffffffffu, up, 31);
+      const int off = start - grp_at < 0x7fffffff ? static_cast<int>(start - grp_at) : 0x7fffffff;
+      const uint32_t hit = __ballot_sync(0xffffffffu, up - len <= off && off < up);
+      if (hit) {
+        const int from = __ffs(hit) - 1;
+        grp = c0 + 32 * i + from;
+        grp_tiles = __shfl_sync(0xffffffffu, mine[i], from);
+        grp_at += __shfl_sync(0xffffffffu, up - len, from);
+      } else {
+        grp_at += __shfl_sync(0xffffffffu, up, 31);
+      }
     }
   }
   if (grp < 0) return;  // more CTAs than runs
   const long long end = pos + per < total ? pos + per : total;  // of a run of tiles
 
   Segment seg;  // the next one to work on; s_seg holds the one in work
-  seg.vis = visible_tiles(a, a.sel ? grp / a.Hkv : grp);
+  seg.vis = visible_tiles(a, load_bounds(a, a.sel ? grp / a.Hkv : grp));
   seg.n = grp_tiles;
   auto place = [&]() {  // the unit at pos of group grp
     const uint32_t off = static_cast<uint32_t>(pos - grp_at);
@@ -468,7 +477,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   auto prologue = [&](const Segment& s) {  // the unit's queries and first copies are on their way
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = (rg * NT + nt) * 8 + g, rr = row < rows ? row : 0, t = rr / a.G;
+      const int row = (rg * NT + nt) * 8 + g, rr = row < rows ? row : 0, t = rr >> a.gsh;
       const bf16* qp = a.q + ((static_cast<size_t>(s.b) * a.T + t) * a.Hq + s.h * a.G + rr - t * a.G) * D;
       if constexpr (Q4) {
 #pragma unroll
@@ -514,7 +523,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
     float qsum[NT][2], qdown[NT][2], qc[NT][4];  // 4 bits, the lane's columns: (Σ q)·factor, factor/2^k, −8·Σ q·2^k (twice)
     auto row_position = [&](int nt, int e) {
       const int row = (rg * NT + nt) * 8 + 2 * t4 + e;
-      return now.vis.L - a.T + (row < rows ? row : 0) / a.G;
+      return now.vis.L - a.T + ((row < rows ? row : 0) >> a.gsh);
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -524,7 +533,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
         qd[nt][e] = 0;
         if (a.slopes) {
           const int row = (rg * NT + nt) * 8 + 2 * t4 + e, rr = row < rows ? row : 0;
-          const float sl = a.slopes[now.h * a.G + rr % a.G];
+          const float sl = a.slopes[now.h * a.G + (rr & (a.G - 1))];
           const int i = row_position(nt, e);
           slope2[nt][e] = sl * kLog2e;
           qd[nt][e] = i - ref_distance(sl, i, ref) - g;
@@ -1133,7 +1142,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           grp_at += static_cast<long long>(seg.n) * mult;
           ++grp;
           seg.n = group_tiles(a, grp);
-          seg.vis = visible_tiles(a, a.sel ? grp / a.Hkv : grp);
+          seg.vis = visible_tiles(a, load_bounds(a, a.sel ? grp / a.Hkv : grp));
         }
         place();
         prologue(seg);
@@ -1175,54 +1184,56 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           to[merge_at<D, Q4>(Q4 ? D / 8 * g + MT + j : 16 * j + 8 + g)] = o[j][nt][2 + e] * by;
         }
       }
-    __syncthreads();
     const bool entire = now.t0 == 0 && now.t1 == now.n;
     const int slot = 2 * blockIdx.x + (first_segment ? 0 : 1);
-    for (int i = tid; i < rows * (D / 4); i += Sh::threads) {
-      const int row = i / (D / 4), c = (i - row * (D / 4)) * 4, r = row / (8 * NT), in = row - r * (8 * NT);
-      float top = -INFINITY;
+    if (tid < rows) {  // one thread per row: its maximum and sum, and where they go
+      const int r = tid / (8 * NT), in = tid - r * (8 * NT);
+      float top = -INFINITY, den = 0.f, cc = 0.f;
 #pragma unroll
       for (int s = 0; s < NS; ++s) top = fmaxf(top, s_m[s * R + r][in]);
-      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-      float den = 0.f, cc = 0.f;
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         const int w = s * R + r;
-        const float* from = red + (w * 8 * NT + in) * PITCH + merge_at<D, Q4>(c);
-        const float4 x = Q4 ? make_float4(from[0], from[1], from[2], from[3]) : *reinterpret_cast<const float4*>(from);
         const float f = s_m[w][in] > -INFINITY ? ex2(s_m[w][in] - top) : 0.f;
-        sum.x += x.x;
-        sum.y += x.y;
-        sum.z += x.z;
-        sum.w += x.w;
         den = fmaf(s_l[w][in], f, den);
         cc = fmaf(s_c[w][in], f, cc);
       }
-      if constexpr (Q4) {
-        sum.x += cc;
-        sum.y += cc;
-        sum.z += cc;
-        sum.w += cc;
-      }
       if (entire) {
-        const int t = row / a.G, hq = now.h * a.G + row - t * a.G;
-        const size_t orow = (static_cast<size_t>(now.b) * a.T + t) * a.Hq + hq;
         const bool none = top == -INFINITY && den == den;  // no visible token with a score above −inf
-        const float by = none ? 0.f : 1.f / den;
-        *reinterpret_cast<float4*>(a.out + orow * D + c) =
-            none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(sum.x * by, sum.y * by, sum.z * by, sum.w * by);
-        if (c == 0 && a.lse) {
+        s_row[tid] = make_float2(none ? 0.f : 1.f / den, cc);
+        if (a.lse) {
+          const int t = tid >> a.gsh, hq = now.h * a.G + tid - (t << a.gsh);
           float lse = none ? -INFINITY : (top + log2f(den)) * kLn2;
           if (a.slopes && !none) {
             const float sl = a.slopes[hq];
             lse -= sl * static_cast<float>(ref_distance(sl, now.vis.L - a.T + t, ref));
           }
-          a.lse[orow] = lse;
+          a.lse[(static_cast<size_t>(now.b) * a.T + t) * a.Hq + hq] = lse;
         }
       } else {
-        *reinterpret_cast<float4*>(a.part + (static_cast<size_t>(slot) * rows + row) * D + c) = sum;
-        if (c == 0) a.ml[static_cast<size_t>(slot) * rows + row] = make_float2(top, den);
+        s_row[tid] = make_float2(1.f, cc);
+        a.ml[static_cast<size_t>(slot) * rows + tid] = make_float2(top, den);
       }
+    }
+    __syncthreads();
+#pragma unroll 2
+    for (int i = tid; i < rows * (D / 4); i += Sh::threads) {
+      const int row = i / (D / 4), c = (i - row * (D / 4)) * 4, r = row / (8 * NT), in = row - r * (8 * NT);
+      const float2 by = s_row[row];
+      float4 sum = Q4 ? make_float4(by.y, by.y, by.y, by.y) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const float* from = red + ((s * R + r) * 8 * NT + in) * PITCH + merge_at<D, Q4>(c);
+        const float4 x = Q4 ? make_float4(from[0], from[1], from[2], from[3]) : *reinterpret_cast<const float4*>(from);
+        sum.x += x.x;
+        sum.y += x.y;
+        sum.z += x.z;
+        sum.w += x.w;
+      }
+      const int t = row >> a.gsh, hq = now.h * a.G + row - (t << a.gsh);
+      float* to = entire ? a.out + ((static_cast<size_t>(now.b) * a.T + t) * a.Hq + hq) * D + c
+                         : a.part + (static_cast<size_t>(slot) * rows + row) * D + c;
+      *reinterpret_cast<float4*>(to) = make_float4(sum.x * by.x, sum.y * by.x, sum.z * by.x, sum.w * by.x);
     }
     if (!entire && tid == 0) {
       a.ref[slot] = ref;
@@ -1256,7 +1267,7 @@ __global__ void __launch_bounds__(kMerge) mod_combine_kernel(ModArgs a) {
   const int item = blockIdx.y * kMerge + threadIdx.x - sl * items;
   const bool live = sl < slices && item < items;
   const int row = live ? item / (D / 4) : 0, c = (item % (D / 4)) * 4, cta = blockIdx.x, n = cut.z;
-  const int b = cut.x / a.Hkv, h = cut.x - b * a.Hkv, t = row / a.G, hq = h * a.G + row - t * a.G;
+  const int b = cut.x / a.Hkv, h = cut.x - b * a.Hkv, t = row >> a.gsh, hq = h * a.G + row - (t << a.gsh);
   auto slot = [&](int p) { return static_cast<size_t>(p == 0 ? cut.y : 2 * (cta + p)); };
   float slope = 0.f;
   int qpos = 0, base = 0;
@@ -1397,6 +1408,7 @@ cudaError_t launch_softmax_mod(const ekv_cache& c, const void* pool, const ekv_s
   a.Hkv = c.num_kv_heads;
   a.Hq = Hq;
   a.G = Hq / c.num_kv_heads;
+  while ((1 << a.gsh) < a.G) ++a.gsh;
   a.T = T;
   a.S = c.page_size;
   a.num_phys = c.num_phys_pages;
