@@ -333,7 +333,8 @@ typedef struct {
  * visible token are read.  A row without a visible token (also L_b = 0, an
  * idle slot, and i < 0) gives out 0 and lse −inf.  K and V of tokens that a
  * row does not see never reach it, NaN and infinities included.  bf16 caches,
- * G·T ≤ 64; anything else returns EKV_ERR_UNSUPPORTED.  ws:
+ * G·T ≤ 64, max_pages·S·Hkv < 2³⁰ (cap·S < 2³⁰ with sel); anything else returns
+ * EKV_ERR_UNSUPPORTED.  ws:
  * ekv_softmax_mod_workspace_bytes() bytes, 256-byte aligned, for one call at a
  * time; nothing in it outlives the call.
  */

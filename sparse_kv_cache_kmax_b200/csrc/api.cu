@@ -229,6 +229,10 @@ ekv_status softmax_mod(const ekv_cache& c, const void* pool, const ekv_seqs* seq
   if (c.dtype != EKV_BF16 || T > kModMaxRows || Hq / c.num_kv_heads * T > kModMaxRows) return EKV_ERR_UNSUPPORTED;
   // rows of the pools are counted in 32 bits
   if (static_cast<int64_t>(c.num_phys_pages) * c.num_kv_heads * c.page_size > INT32_MAX) return EKV_ERR_UNSUPPORTED;
+  // and the tiles of 32 sequences (of 32 units, when pages are selected)
+  const int64_t tiles = static_cast<int64_t>(sel ? cap : static_cast<int64_t>(seqs->max_pages) * c.num_kv_heads) *
+                        (c.page_size / 16);
+  if (tiles >= 1 << 26) return EKV_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(out) || !aligned16(c.k_pool) || !aligned16(c.v_pool)) return EKV_ERR_INVALID_ARG;
   if (mod != nullptr && (!isfinite(mod->softcap) || mod->softcap < 0.0f || mod->window < 0)) return EKV_ERR_INVALID_ARG;
   EKV_TRY(check_ws(ws, ws_bytes, softmax_mod_ws_bytes(c.head_dim, Hq / c.num_kv_heads * T)));

@@ -347,7 +347,9 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
       int x = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) x += value(mine[i]);
-      total += static_cast<long long>(warp_sum(x)) * mult;
+      // in two halves: 128 long sequences pass 32 bits
+      total += (__reduce_add_sync(0xffffffffu, x & 0xffff) +
+                (static_cast<long long>(__reduce_add_sync(0xffffffffu, x >> 16)) << 16)) * mult;
     }
     return total;
   };

@@ -136,6 +136,16 @@ def test_decode_refuses(n):
     assert _decode(cache=_q4(), **kw) == status
 
 
+def test_decode_refuses_lists_past_32_bits():
+    # 32 sequences of 2²⁶ (token tile, KV head) pairs: their number needs 32 bits and a sign
+    for cache in (_cache(), _q4()):
+        assert _decode(cache=cache, seqs=_seqs(max_pages=2 ** 23), cap=2 ** 23) == UNSUPPORTED
+        assert _decode(cache=cache, sel=FAKE, n_sel=FAKE, cap=2 ** 26) == UNSUPPORTED
+        # one page less passes this check and meets the next
+        assert _decode(cache=cache, seqs=_seqs(max_pages=2 ** 23 - 1), cap=2 ** 23, ws=None) == WORKSPACE
+        assert _decode(cache=cache, sel=FAKE, n_sel=FAKE, cap=2 ** 26 - 1, ws=None) == WORKSPACE
+
+
 def test_decode_refuses_caches():
     assert _decode(cache=_cache(dtype=B.EKV_F32)) == UNSUPPORTED
     assert _decode(cache=_cache(head_dim=256)) == UNSUPPORTED
