@@ -101,7 +101,8 @@ __device__ bool page_item(const A& a, int item, PageItem* out) {
     return false;
   }
   const int first = L - n, p = first / a.S + k;
-  if (k < 0 || p * a.S >= L) return false;
+  // in 64 bits: behind a sequence that ends near 2^31 lie items whose pages start past it
+  if (k < 0 || static_cast<int64_t>(p) * a.S >= L) return false;
   const int phys = a.page_table[static_cast<size_t>(b) * a.max_pages + p];
   if (!phys_ok(phys, a.num_phys)) return false;
   out->phys = phys;

@@ -609,3 +609,36 @@ def test_streams_captures_and_repeats_agree():
     torch.cuda.synchronize()
     assert not torch.equal(first[0][0], out[0][0]) and torch.equal(first[0][1:], out[0][1:])
     assert B.ekv_get_error() == 0
+
+
+@pytest.mark.parametrize("q4", [False, True])
+def test_appends_and_reads_at_the_last_positions(q4):
+    """The longest sequence of 32-bit positions (all of its pages one physical page),
+    with unused rows behind its token: the items of pages past its end do nothing."""
+    d, S, rows, pages = 64, 16, 200, 2 ** 27 - 1
+    L = pages * S
+    g = torch.Generator(device="cuda").manual_seed(9)
+    k, v = (torch.randn(rows, 1, d, generator=g, device="cuda").to(BF) for _ in range(2))
+    seqs = B.make_seqs(torch.zeros(1, pages, dtype=torch.int32, device="cuda"),
+                       torch.tensor([L], dtype=torch.int32, device="cuda"))
+    indptr = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    new = B.make_new_tokens(k, v, indptr=indptr)
+    if not q4:
+        kp, vp = (torch.zeros(1, 1, S, d, dtype=BF, device="cuda") for _ in range(2))
+        c = B.make_cache(kp, vp)
+        c.box = c.mom = None
+        B.ekv_rope_append(c, seqs, None, new)
+        assert torch.equal(kp[0, :, -1], k[0]) and torch.equal(vp[0, :, -1], v[0])
+        assert not kp[0, :, :-1].any() and not vp[0, :, :-1].any()
+    else:
+        pool = torch.zeros(1, 1, 1, 16 * d + 128, dtype=torch.uint8, device="cuda")
+        c = B.make_cache_q4(pool, d)
+        B.ekv_rope_append_q4(c, seqs, None, new)
+        out = [torch.full((rows, 1, d), 7.0, device="cuda") for _ in range(2)]
+        B.ekv_q4_read(c, seqs, indptr, *out)
+        for got, x in zip(out, (k, v)):
+            codes, step, zero = quantise64(np64(x[0, 0]))
+            assert (np64(got[0, 0]) == (zero + step * codes).astype(np.float32)).all() and (got[1:] == 7).all()
+        codes, step, _ = unpack(pool, d)
+        assert not codes[..., :-1, :].any() and not step[..., :-1].any()
+    assert B.ekv_get_error() == 0
