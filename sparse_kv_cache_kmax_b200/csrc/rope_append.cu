@@ -395,97 +395,92 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(AppendArgs a) 
   }
 }
 
-// One row of D numbers, D/32 of them per lane, to codes: the lane's codes come
-// back packed, the pair (step, zero) on every lane.  x: the numbers in fp32,
-// each off by at most err (one bound for the row); exact(e) gives number e in
-// 64 bits.  Nearly every row is decided in fp32: only where step or zero may
-// round to two bf16 numbers, or a quotient is near a border between two codes,
-// are the exact numbers asked (rotated keys: 1 row and 1 number in some ten
-// thousand).  All in 64 bits cost four times the issue slots.
-template <int E, class F>
-__device__ __forceinline__ uint32_t quantise_row(const float (&x)[E], float err, F exact, uint32_t* step_zero) {
-  float mn = x[0], mx = x[0];
-#pragma unroll
-  for (int e = 1; e < E; ++e) {
-    mn = fminf(mn, x[e]);
-    mx = fmaxf(mx, x[e]);
+// A row of numbers, eight to each of W lanes (W a power of two: a warp takes
+// 32/W rows at a time), becomes codes.  Nearly every row is decided in fp32 from
+// numbers x, each off by at most err (one bound for the row): only where step or
+// zero may round to two bf16 numbers, or a quotient is near a border between two
+// codes, are the exact numbers asked, exact(e) in 64 bits (rotated keys: 1 row
+// and 1 number in some ten thousand).  All in 64 bits cost four times the issue
+// slots.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Step and zero, from the row's extremes: as low halves of two words, whose
+// upper halves differ from them where 64 bits have to decide.
+struct Pair {
+  uint32_t step, zero;
+  __device__ __forceinline__ bool unsure() const {
+    return step != __byte_perm(step, 0, 0x1010) || zero != __byte_perm(zero, 0, 0x1010) || !(bf16_lo(step) <= 3e38f);
   }
-  asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(mn) : "f"(mn));
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mx) : "f"(mx));
-  auto pair = [](float a, float b) {
-    const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&r);
-  };
+};
+__device__ __forceinline__ Pair step_zero(float mn, float mx, float err) {
   // step: off by 2·err/15 of the extremes, and three roundings of fp32
-  float step = (mx - mn) * (1.0f / 15.0f);
-  const float es = err * 0.14f + step * 0x1p-22f;
-  uint32_t sw = pair(step - es, step + es), zw = pair(mn - err, mn + err);
-  if (sw != __byte_perm(sw, 0, 0x1010) || zw != __byte_perm(zw, 0, 0x1010) || !(step <= 3e38f)) {
-    double dmn = exact(0), dmx = dmn;
+  const float step = (mx - mn) * (1.0f / 15.0f), es = err * 0.14f + step * 0x1p-22f;
+  return Pair{bf16_pair(step - es, step + es), bf16_pair(mn - err, mn + err)};
+}
+template <int W, class F>
+__device__ __forceinline__ Pair step_zero_exact(F exact) {
+  double mn = exact(0), mx = mn;
 #pragma unroll
-    for (int e = 1; e < E; ++e) {
-      dmn = fmin(dmn, exact(e));
-      dmx = fmax(dmx, exact(e));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      dmn = fmin(dmn, __shfl_xor_sync(0xffffffffu, dmn, o));
-      dmx = fmax(dmx, __shfl_xor_sync(0xffffffffu, dmx, o));
-    }
-    sw = pair(__double2float_rn((dmx - dmn) / 15.0), 0.f);
-    zw = pair(__double2float_rn(dmn), 0.f);
+  for (int e = 1; e < 8; ++e) {
+    mn = fmin(mn, exact(e));
+    mx = fmax(mx, exact(e));
   }
-  step = bf16_lo(sw);
-  const float zero = bf16_lo(zw);
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) {
+    mn = fmin(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+  return Pair{bf16_pair(__double2float_rn((mx - mn) / 15.0), 0.f), bf16_pair(__double2float_rn(mn), 0.f)};
+}
+// The lane's codes, packed; *packed: the row's (step, zero) as they are stored.
+template <class F>
+__device__ __forceinline__ uint32_t row_codes(const float (&x)[8], Pair p, float err, F exact, uint32_t* packed) {
+  float step = bf16_lo(p.step);
+  const float zero = bf16_lo(p.zero);
   if (!(step >= 1e-30f)) step = 0.f;
-  const float inv = step > 0.f ? 1.0f / step : 0.f, off = -zero * inv;
-  // codes: f is off by err·inv and by the roundings of inv, off and the sum,
-  // 2⁻²⁴·(3·|off| + 48) at most; adding 1.5·2²³ rounds it to a whole number in
-  // the low bits
+  // f = (x − zero)/(15·step), clamped to 0 .. 1 as it is formed.  15·f ≤ 15 is off
+  // by 15·err·inv, by 2⁻²³ of it for the reciprocal and 2⁻²⁴ for each of 1/15, the
+  // product and f (75·2⁻²⁴ < 5e-6), and by 15·2⁻²⁴ of |off| for the rounding of
+  // off; adding 1.5·2²³ rounds it to a whole number in the low bits.
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(step));
+  inv = step > 0.f ? inv * (1.0f / 15.0f) : 0.f;
+  const float off = -zero * inv;
   uint32_t codes = 0;
   float worst = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float f = fminf(fmaxf(fmaf(x[e], inv, off), 0.f), 15.f), t = f + 12582912.f;
-    worst = fmaxf(worst, fabsf(f - (t - 12582912.f)));
-    codes += (__float_as_uint(t) - 0x4b400000u) << (4 * e);
+  for (int e = 0; e < 8; ++e) {
+    const float f = __saturatef(fmaf(x[e], inv, off)), t = fmaf(f, 15.f, 12582912.f);
+    worst = fmaxf(worst, fabsf(fmaf(f, 15.f, 12582912.f - t)));
+    codes += __float_as_uint(t) << (4 * e);
   }
-  if (!(worst <= 0.5f - 4e-6f - fabsf(off) * 2e-7f - err * inv) && step > 0.f) {
+  codes -= 0x4b400000u * 0x11111111u;  // eight times the bits of 1.5·2²³
+  // (above 2^120 the reciprocal is near the end of its range)
+  if (!(worst <= 0.5f - 5e-6f - fabsf(off) * 3e-6f - 15.f * err * inv && step <= 0x1p120f) && step > 0.f) {
     // the code below (a quotient that slips past a whole number changes nothing),
     // and the exact border above it: (n + ½)·step has 13 bits
     codes = 0;
+    const double by = static_cast<double>(1.0f / step);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
+    for (int e = 0; e < 8; ++e) {
       const double d = exact(e) - static_cast<double>(zero);
-      const float n = floorf(fminf(fmaxf(__double2float_rn(d * static_cast<double>(inv)), 0.f), 15.f));
+      const float n = floorf(fminf(fmaxf(__double2float_rn(d * by), 0.f), 15.f));
       const double border = static_cast<double>((n + 0.5f) * step);
       const int k = static_cast<int>(n);
       codes |= static_cast<uint32_t>(min(15, k + (d > border || (d == border && (k & 1)) ? 1 : 0))) << (4 * e);
     }
   }
-  *step_zero = (__float_as_uint(step) >> 16) | (__float_as_uint(zero) & 0xffff0000u);
+  *packed = (__float_as_uint(step) >> 16) | (__float_as_uint(zero) & 0xffff0000u);
   return codes;
 }
 
-template <typename T, int E>
-__device__ __forceinline__ void load_lane(const T* p, float (&v)[E]) {
-  if constexpr (E == 4) {
-    load4(p, v);
-  } else if constexpr (sizeof(T) == 2) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-    v[0] = bf16_lo(w);
-    v[1] = bf16_hi(w);
-  } else {
-    const float2 w = *reinterpret_cast<const float2*>(p);
-    v[0] = w.x;
-    v[1] = w.y;
-  }
-}
-
-// grid as rope_append_kernel; a warp takes one token's K and V at a time, D/32
-// numbers of each per lane.  A key's exact rotated numbers, where they are
-// asked for: the products are exact in 64 bits (24 + 24 bits), so their sum is
-// rounded once, at 2⁻⁵³.
+// grid as rope_append_kernel; a warp takes the K and V of 256/D tokens at a time,
+// eight numbers of each per lane, so that what is worked out once per row is
+// shared by two tokens (four of d = 64).  A key's exact rotated numbers, where they
+// are asked for: the products are exact in 64 bits (24 + 24 bits), so their sum
+// is rounded once, at 2⁻⁵³.
 template <typename T, int D, int S>
 __global__ void __launch_bounds__(kThreads, 5) rope_append_q4_kernel(AppendArgs a) {
   grid_dep_enter();
@@ -497,39 +492,31 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_q4_kernel(AppendArgs 
     rotate_queries<T, D>(a, it, h0, h1);
     return;
   }
-  constexpr int E = D / 32, R = q4_record_bytes(D), kRow = D / 2, kWarps = kThreads / 32;
+  constexpr int R = q4_record_bytes(D), kRow = D / 2, kLanes = D / 8, kToks = 32 / kLanes, kPass = kThreads / kLanes;
   __shared__ __align__(16) unsigned char codes_s[S * kRow];
   __shared__ uint32_t sz_s[S];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = it.hi - it.lo;
-  const int j = lane * E, half = a.rot / 2;
+  const int lane = threadIdx.x & 31, in_row = lane % kLanes, n = it.hi - it.lo;
+  const int first = static_cast<int>(threadIdx.x) / 32 * kToks, mine = lane / kLanes;  // a warp's first token, the lane's
+  const int j = in_row * 8, half = a.rot / 2;
   // this lane's partners and angles: number j + e pairs with j + e + half, − half, or its neighbour
-  const bool turns = j < a.rot, low = a.interleaved || j < half;
+  const bool turns = j < a.rot, low = j < half;
   const int other = !turns || a.interleaved ? j : (low ? j + half : j - half);
-  const int angle = a.interleaved ? j / 2 : (low ? j : j - half);
   struct Numbers {
-    float x[E], z[E], v[E], c[E], s[E];
+    uint4 x[sizeof(T) / 2], z[sizeof(T) / 2], v[sizeof(T) / 2];
   };
-  auto load = [&](Numbers& m, int h, int t) {
-    const T* ksrc = static_cast<const T*>(a.k) + (it.row + t) * a.k_stride + h * D;
-    load_lane<T, E>(ksrc + j, m.x);
-    load_lane<T, E>(ksrc + other, m.z);
-    load_lane<T, E>(static_cast<const T*>(a.v) + (it.row + t) * a.v_stride + h * D + j, m.v);
-    if (turns) {
-      const float* cs = rotation_row(a, it.pos + it.lo + t);
-      if (a.interleaved) {
+  auto load = [&](Numbers& m, int h, int t0) {
+    const int64_t row = it.row + min(t0 + mine, n - 1);
+    const T* ksrc = static_cast<const T*>(a.k) + row * a.k_stride + h * D;
+    const T* vsrc = static_cast<const T*>(a.v) + row * a.v_stride + h * D;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          m.c[e] = m.c[e + 1] = cs[angle + e / 2];
-          m.s[e] = m.s[e + 1] = cs[half + angle + e / 2];
-        }
-      } else {
-        load_lane<float, E>(cs + angle, m.c);
-        load_lane<float, E>(cs + half + angle, m.s);
-      }
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
+      m.x[i] = reinterpret_cast<const uint4*>(ksrc + j)[i];
+      m.z[i] = reinterpret_cast<const uint4*>(ksrc + other)[i];
+      m.v[i] = reinterpret_cast<const uint4*>(vsrc + j)[i];
     }
   };
   Numbers next;
-  if (warp < n) load(next, h0, warp);
+  if (first < n) load(next, h0, first);
   for (int h = h0; h < h1; ++h) {
     unsigned char* page = static_cast<unsigned char*>(a.k_pool) +
                           (static_cast<size_t>(it.phys) * a.Hkv + h) * (S / kTile) * R;
@@ -543,51 +530,88 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_q4_kernel(AppendArgs 
       for (int slot = threadIdx.x; slot < it.lo; slot += kThreads)
         sz_s[slot] = reinterpret_cast<const uint32_t*>(page + (slot / kTile) * R + 16 * D)[slot % kTile];
     }
-    for (int t = warp; t < n; t += kWarps) {
-      const int slot = it.lo + t;
-      float x[E], z[E], v[E], c[E], s[E];
+    for (int t0 = first; t0 < n; t0 += kPass) {
+      const int t = min(t0 + mine, n - 1), slot = it.lo + t;
+      float c[8], s[8];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        x[e] = next.x[e];
-        v[e] = next.v[e];
-        z[e] = a.interleaved ? next.z[e ^ 1] : next.z[e];  // the pair's other number
-        c[e] = turns ? next.c[e] : 1.f;
-        s[e] = turns ? next.s[e] : 0.f;
+      for (int e = 0; e < 8; ++e) {
+        c[e] = 1.f;
+        s[e] = 0.f;
       }
-      if (t + kWarps < n) load(next, h, t + kWarps);  // in flight during this token's work
-      else if (h + 1 < h1) load(next, h + 1, warp);
-      // number e: x·c − z·s for the first of a pair, x·c + z·s for the second
+      if (turns) {  // number e: x·c − z·s for the first of a pair, x·c + z·s for the second
+        const float* cs = rotation_row(a, it.pos + slot);
+        if (a.interleaved) {
+          float c4[4], s4[4];
+          load4(cs + j / 2, c4);
+          load4(cs + half + j / 2, s4);
 #pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (a.interleaved ? (e & 1) == 0 : low) s[e] = -s[e];
-      float y[E], big = 0.f;
+          for (int e = 0; e < 8; ++e) {
+            c[e] = c4[e / 2];
+            s[e] = e & 1 ? s4[e / 2] : -s4[e / 2];
+          }
+        } else {
+          const int angle = low ? j : j - half;
+          load8(cs + angle, c);
+          load8(cs + half + angle, s);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        y[e] = fmaf(x[e], c[e], z[e] * s[e]);
-        big = fmaxf(big, fabsf(y[e]) + fabsf(z[e] * s[e]));
+          for (int e = 0; e < 8; ++e) s[e] = low ? -s[e] : s[e];
+        }
       }
-      asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(big) : "f"(big));
+      const Numbers now = next;
+      if (t0 + kPass < n) load(next, h, t0 + kPass);  // in flight during this token's work
+      else if (h + 1 < h1) load(next, h + 1, first);
+      float x[8], z[8], v[8];
+      widen8<T>(now.x, x);
+      widen8<T>(now.z, z);
+      if (a.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          const float y = z[e];
+          z[e] = z[e + 1];
+          z[e + 1] = y;
+        }
+      }
+      widen8<T>(now.v, v);
+      // numbers, extremes, and what the rotation's two roundings may be off by
+      float y[8], big = 0.f, kmn, kmx, vmn, vmx;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float zs = z[e] * s[e];
+        y[e] = fmaf(x[e], c[e], zs);
+        big = fmaxf(big, fabsf(y[e]) + fabsf(zs));
+        kmn = e ? fminf(kmn, y[e]) : y[e];
+        kmx = e ? fmaxf(kmx, y[e]) : y[e];
+        vmn = e ? fminf(vmn, v[e]) : v[e];
+        vmx = e ? fmaxf(vmx, v[e]) : v[e];
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) {
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        kmn = fminf(kmn, __shfl_xor_sync(0xffffffffu, kmn, o));
+        kmx = fmaxf(kmx, __shfl_xor_sync(0xffffffffu, kmx, o));
+        vmn = fminf(vmn, __shfl_xor_sync(0xffffffffu, vmn, o));
+        vmx = fmaxf(vmx, __shfl_xor_sync(0xffffffffu, vmx, o));
+      }
+      const float err = a.rot ? big * 0x1.1p-24f : 0.f;
+      auto key = [&](int e) {
+        return static_cast<double>(x[e]) * static_cast<double>(c[e]) +
+               static_cast<double>(z[e]) * static_cast<double>(s[e]);
+      };
+      auto value = [&](int e) { return static_cast<double>(v[e]); };
+      Pair kp = step_zero(kmn, kmx, err), vp = step_zero(vmn, vmx, 0.f);
+      if (__any_sync(0xffffffffu, kp.unsure() || vp.unsure())) {
+        kp = step_zero_exact<kLanes>(key);
+        vp = step_zero_exact<kLanes>(value);
+      }
       uint32_t ksz, vsz;
-      const uint32_t kc = quantise_row<E>(
-          y, a.rot ? big * 0x1.1p-24f : 0.f,
-          [&](int e) {
-            return static_cast<double>(x[e]) * static_cast<double>(c[e]) +
-                   static_cast<double>(z[e]) * static_cast<double>(s[e]);
-          },
-          &ksz);
-      const uint32_t vc = quantise_row<E>(v, 0.f, [&](int e) { return static_cast<double>(v[e]); }, &vsz);
+      const uint32_t kc = row_codes(y, kp, err, key, &ksz), vc = row_codes(v, vp, 0.f, value, &vsz);
+      if (t0 + mine >= n) continue;
       unsigned char* rec = page + (slot / kTile) * R;
       const int r = slot % kTile;
-      if constexpr (E == 4) {
-        reinterpret_cast<uint16_t*>(rec + r * kRow)[lane] = static_cast<uint16_t>(kc);
-        reinterpret_cast<uint16_t*>(rec + (kTile + r) * kRow)[lane] = static_cast<uint16_t>(vc);
-        reinterpret_cast<uint16_t*>(codes_s + slot * kRow)[lane] = static_cast<uint16_t>(kc);
-      } else {
-        rec[r * kRow + lane] = static_cast<unsigned char>(kc);
-        rec[(kTile + r) * kRow + lane] = static_cast<unsigned char>(vc);
-        codes_s[slot * kRow + lane] = static_cast<unsigned char>(kc);
-      }
-      if (lane == 0) {
+      reinterpret_cast<uint32_t*>(rec + r * kRow)[in_row] = kc;
+      reinterpret_cast<uint32_t*>(rec + (kTile + r) * kRow)[in_row] = vc;
+      reinterpret_cast<uint32_t*>(codes_s + slot * kRow)[in_row] = kc;
+      if (in_row == 0) {
         reinterpret_cast<uint32_t*>(rec + 16 * D)[r] = ksz;
         reinterpret_cast<uint32_t*>(rec + 16 * D)[kTile + r] = vsz;
         sz_s[slot] = ksz;
