@@ -649,45 +649,74 @@ struct ReadArgs {
   int heads;  // KV heads that one CTA takes in turn
 };
 
-// grid: (items, CTAs of a.heads KV heads); a thread turns eight codes (one
-// word) of K and of V into values, two tokens of each at a time.  Bound by the
-// values' writes.
+// grid: (items, CTAs of a.heads KV heads); a thread turns as many codes of K and
+// of V into values as 16 bytes hold, so that a warp's stores are one block, two
+// tokens of each at a time.  Bound by the values' writes (eight fp32 values per
+// thread, in two stores 32 bytes apart, took 240 us for 128k tokens, this 207).
+template <typename T>
+struct CodesOf {
+  using type = uint32_t;
+};
+template <>
+struct CodesOf<float> {
+  using type = uint16_t;
+};
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) q4_read_kernel(ReadArgs a) {
   grid_dep_enter();
   PageItem it;
   if (!page_item(a, blockIdx.x, &it)) return;
-  constexpr int R = q4_record_bytes(D), kWords = D / 8, kRows = kThreads / kWords;
+  using Codes = typename CodesOf<T>::type;
+  constexpr int E = 16 / sizeof(T), R = q4_record_bytes(D), kWords = D / E, kRows = kThreads / kWords;
   const int w = threadIdx.x % kWords, n = it.hi - it.lo;
   const int h1 = min(a.Hkv, (static_cast<int>(blockIdx.y) + 1) * a.heads);
-  for (int h = blockIdx.y * a.heads; h < h1; ++h) {
+  // a step: two tokens of one head.  Its codes are loaded while the step before
+  // is turned into values.
+  struct Step {
+    uint32_t codes[2][2], sz[2][2];
+  };
+  const int first = threadIdx.x / kWords;
+  auto load = [&](Step& s, int h, int t0) {
     const unsigned char* page = a.pool + (static_cast<size_t>(it.phys) * a.Hkv + h) * (a.S / kTile) * R;
-    for (int t0 = threadIdx.x / kWords; t0 < n; t0 += 2 * kRows) {
-      uint32_t codes[2][2], sz[2][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int slot = it.lo + min(t0 + i * kRows, n - 1);
-        const unsigned char* rec = page + (slot / kTile) * R;
+    for (int i = 0; i < 2; ++i) {
+      const int slot = it.lo + min(t0 + i * kRows, n - 1);
+      const unsigned char* rec = page + (slot / kTile) * R;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int r = v * kTile + slot % kTile;
-          codes[i][v] = reinterpret_cast<const uint32_t*>(rec + r * (D / 2))[w];
-          sz[i][v] = reinterpret_cast<const uint32_t*>(rec + 16 * D)[r];
-        }
+      for (int v = 0; v < 2; ++v) {
+        const int r = v * kTile + slot % kTile;
+        s.codes[i][v] = reinterpret_cast<const Codes*>(rec + r * (D / 2))[w];
+        s.sz[i][v] = reinterpret_cast<const uint32_t*>(rec + 16 * D)[r];
       }
+    }
+  };
+  int h = blockIdx.y * a.heads, t0 = first;
+  if (t0 >= n) return;
+  Step next;
+  load(next, h, t0);
+  while (h < h1) {
+    const Step now = next;
+    const int h_now = h, t_now = t0;
+    t0 += 2 * kRows;
+    if (t0 >= n) {
+      t0 = first;
+      ++h;
+    }
+    if (h < h1) load(next, h, t0);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = t0 + i * kRows;
-        if (t >= n) continue;
+    for (int i = 0; i < 2; ++i) {
+      const int t = t_now + i * kRows;
+      if (t >= n) continue;
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          T* to = static_cast<T*>(v ? a.v_out : a.k_out);
-          if (to == nullptr) continue;
-          float x[8];
+      for (int v = 0; v < 2; ++v) {
+        T* to = static_cast<T*>(v ? a.v_out : a.k_out);
+        if (to == nullptr) continue;
+        float x[E];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = q4_value(sz[i][v], (codes[i][v] >> (4 * e)) & 15u);
-          store8(to + (static_cast<int64_t>(it.row + t) * a.Hkv + h) * D + 8 * w, x);
-        }
+        for (int e = 0; e < E; ++e) x[e] = q4_value(now.sz[i][v], (now.codes[i][v] >> (4 * e)) & 15u);
+        to += (static_cast<int64_t>(it.row + t) * a.Hkv + h_now) * D + E * w;
+        if constexpr (E == 8) store8(to, x);
+        else *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
       }
     }
   }
@@ -697,15 +726,16 @@ int item_count(const int32_t* indptr, int rows, int batch, int S) {
   return indptr == nullptr ? batch : rows / S + 2 * batch;
 }
 
-// KV heads per CTA: one while items × heads are within the given waves of five
-// CTAs per SM (a decode step, a short chunk: latency), else as many as keep to
-// them (long prompts: the page lookups, metadata tails and launches of ten times
-// as many CTAs cost more than the waves' ends).  Measured on 15k new tokens of 8
-// KV heads: two waves 75.7 us, four 79.6, one head per CTA 84; read-back of 100k
-// tokens of 4-bit cache: four waves 96.9 us, two 97.1, but 4k tokens 15.3 and 17.7.
+// KV heads per CTA: about as many as keep the launch to the given waves of five
+// CTAs per SM, at least one.  A decode step or a short chunk has one head per
+// CTA (latency); in long prompts the page lookups, metadata tails and launches
+// of ten times as many CTAs cost more than the waves' ends.  Measured: 15k new
+// tokens of 8 KV heads, one head per CTA 84 us, four waves 74.8, two 73.0; the
+// read-back of 16k tokens with six waves 19.7, four 16.5, three 15.2, two 15.1, of
+// 32k with three 31.2 and two 33.6.
 int heads_per_cta(int items, int Hkv, int waves) {
   const int64_t room = 5ll * waves * sm_count();
-  const int64_t h = static_cast<int64_t>(items) * Hkv / (room > 0 ? room : 1);
+  const int64_t h = (static_cast<int64_t>(items) * Hkv + room / 2) / (room > 0 ? room : 1);
   return static_cast<int>(h < 1 ? 1 : (h > Hkv ? Hkv : h));
 }
 
@@ -781,7 +811,7 @@ cudaError_t launch_q4_read(const ekv_cache_q4& c, const ekv_seqs& s, const int32
              k_out,        v_out,          s.batch,     num_tokens,
              c.num_kv_heads, c.page_size,  c.num_phys_pages, s.max_pages, 1};
   const int items = item_count(indptr, num_tokens, s.batch, c.page_size);
-  a.heads = heads_per_cta(items, c.num_kv_heads, 4);
+  a.heads = heads_per_cta(items, c.num_kv_heads, 3);
   const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>((c.num_kv_heads + a.heads - 1) / a.heads));
   const bool wide = c.head_dim == 128;
   if (out_dtype == EKV_BF16)
