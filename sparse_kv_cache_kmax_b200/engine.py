@@ -68,7 +68,8 @@ class DecodeEngine:
         pages they touch.  Returns q [tokens, Hq, d] rotated alike (q without a
         table, None without q)."""
         turn = q is not None and self.rope is not None
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if turn else None
+        with torch.cuda.stream(stream):  # memory that other streams do not take back too early
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if turn else None
         B.ekv_rope_append(self.cache, self.seqs, self.rope,
                           B.make_new_tokens(k, v, q if turn else None, out, indptr), stream)
         return out if turn else q
@@ -126,8 +127,9 @@ def _softmax(call, eng, q, sel, n_sel, cap, mod, stream):
         if nbytes == 0:
             raise ValueError("unsupported heads or query tokens")
         ws = eng.mod_ws[T] = B.workspace(nbytes, eng.device)
-    out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
     call(eng.cache, eng.seqs, q, eng.scale, B.make_score_mod(**mod), sel, n_sel, cap, out, ws, lse=lse, stream=stream)
     return out, lse
 
@@ -167,7 +169,8 @@ class Q4Engine:
     def append(self, k, v, q=None, indptr=None, stream=None):
         """As DecodeEngine.append, into the 4-bit cache."""
         turn = q is not None and self.rope is not None
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if turn else None
+        with torch.cuda.stream(stream):  # memory that other streams do not take back too early
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if turn else None
         B.ekv_rope_append_q4(self.cache, self.seqs, self.rope,
                              B.make_new_tokens(k, v, q if turn else None, out, indptr), stream)
         return out if turn else q
@@ -200,7 +203,8 @@ class Q4Engine:
     def read(self, indptr, tokens, dtype=torch.bfloat16, stream=None):
         """The last tokens of every sequence as values: (k, v) [tokens, Hkv, d],
         rows by indptr."""
-        k = torch.zeros(tokens, self.Hkv, self.d, dtype=dtype, device=self.device)
-        v = torch.zeros_like(k)
+        with torch.cuda.stream(stream):  # the zeros come first on it
+            k = torch.zeros(tokens, self.Hkv, self.d, dtype=dtype, device=self.device)
+            v = torch.zeros_like(k)
         B.ekv_q4_read(self.cache, self.seqs, indptr, k, v, stream)
         return k, v

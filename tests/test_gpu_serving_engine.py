@@ -143,3 +143,35 @@ def test_engine_refusals():
         eng.softmax(q, slopes=torch.zeros(3, device="cuda"))
     with pytest.raises(ValueError):
         eng.append(torch.zeros(1, 2, 64, device="cuda"), torch.zeros(1, 2, 64, device="cuda"))
+
+
+def test_another_stream_than_the_current_one():
+    """What an engine allocates for a call belongs to the call's stream: its zeros come
+    before the rows, and nobody gets a rotated q's memory while a step still reads it."""
+    pg, table, q, k, v = _program(16, 77)
+    lens = torch.tensor(PROMPTS, dtype=torch.int32, device="cuda")
+    engines = [Q4Engine(Q4Engine.new_pool(pg.n_phys, HKV, 16, D, "cuda"), D, pg.table, lens, HKV * G, cos_sin=table)
+               for _ in range(2)]
+    ks, vs, ip = _rows(k, PROMPTS, PROMPTS), _rows(v, PROMPTS, PROMPTS), _indptr(PROMPTS)
+    for e in engines:
+        e.append(ks, vs, None, ip)
+    want = engines[0].read(ip, sum(PROMPTS))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(40_000_000)                     # the current stream is behind
+    got = engines[1].read(ip, sum(PROMPTS), stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+    after, new = [p + 1 for p in PROMPTS], [1] * len(PROMPTS)
+    lens.copy_(torch.tensor(after, dtype=torch.int32))
+    qs, k1, v1 = (_rows(x, after, new) for x in (q, k, v))
+    out, lse = engines[0].step(qs, k1, v1)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)                 # the step's stream is behind
+    out2, lse2 = engines[1].step(qs, k1, v1, stream=side)
+    other = [torch.full_like(qs, float("nan")) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, out2) and torch.equal(lse, lse2) and len(other) == 4
+    assert B.ekv_get_error() == 0
