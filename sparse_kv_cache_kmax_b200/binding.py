@@ -201,8 +201,11 @@ def make_seqs(page_table, seq_lens) -> Seqs:
     """page_table: int32 [B, max_pages]; seq_lens: int32 [B] (device)."""
     if page_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise ValueError("page_table and seq_lens must be int32")
+    if not page_table.is_contiguous() or not seq_lens.is_contiguous():
+        raise ValueError("page_table and seq_lens must be contiguous")
+    _same_device(page_table, seq_lens)
     s = Seqs(page_table.data_ptr(), seq_lens.data_ptr(), page_table.shape[0], page_table.shape[1])
-    s._keep = (page_table.contiguous(), seq_lens.contiguous())
+    s._keep, s.device_index = (page_table, seq_lens), page_table.get_device()
     return s
 
 
@@ -258,7 +261,7 @@ def make_new_tokens(k, v, q=None, q_out=None, indptr=None) -> NewTokens:
     for t in rows:
         if t.dtype != k.dtype or t.dtype not in _DTYPES or t.shape[0] != k.shape[0] or t.shape[2] != k.shape[2]:
             raise ValueError("q, k, v and q_out must share their type, tokens and head size")
-        if t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+        if t.stride(2) != 1 or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
             raise ValueError("the heads of a token must be dense")
     if q is not None and (q.shape != q_out.shape or not q_out.is_contiguous()):
         raise ValueError("q_out must be dense, of q's shape")
@@ -266,8 +269,9 @@ def make_new_tokens(k, v, q=None, q_out=None, indptr=None) -> NewTokens:
         raise ValueError("indptr must be int32 [batch + 1]")
     _same_device(*rows, *([] if indptr is None else [indptr]))
     pq = (lambda t: 0 if t is None else t.data_ptr())
-    n = NewTokens(pq(q), k.data_ptr(), v.data_ptr(), pq(q_out), 0 if q is None else q.stride(0), k.stride(0),
-                  v.stride(0), pq(indptr), k.shape[0], 0 if q is None else q.shape[1], _DTYPES[k.dtype])
+    stride = (lambda t: 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2])
+    n = NewTokens(pq(q), k.data_ptr(), v.data_ptr(), pq(q_out), stride(q), stride(k), stride(v), pq(indptr), k.shape[0],
+                  0 if q is None else q.shape[1], _DTYPES[k.dtype])
     n._keep, n.device_index, n.heads = (rows, indptr), k.get_device(), (k.shape[1], k.shape[2])
     n.sequences = None if indptr is None else indptr.numel() - 1
     return n
@@ -404,7 +408,7 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 # microseconds: what can be checked once is checked where the descriptions are
 # made, and a call compares integers.
 def _check_append(device, heads, seqs, rope, new):
-    if new.device_index != device or (rope is not None and rope.device_index != device):
+    if new.device_index != device or seqs.device_index != device or (rope is not None and rope.device_index != device):
         raise ValueError("all tensors must be on one device")
     _on_current(device)
     if new.heads != heads:
@@ -449,6 +453,8 @@ def ekv_q4_read(cache, seqs, indptr, k_out=None, v_out=None, stream=None):
     for t in (k_out, v_out, indptr):
         if t is not None and not (t.is_contiguous() and t.get_device() == device):
             raise ValueError("k_out, v_out and indptr must be dense, on the cache's device")
+    if seqs.device_index != device:
+        raise ValueError("all tensors must be on one device")
     _on_current(device)
     st = lib().ekv_q4_read(cache, seqs, indptr.data_ptr(), shape[0], dt, None if k_out is None else k_out.data_ptr(),
                            None if v_out is None else v_out.data_ptr(), _raw_stream(stream, device))
@@ -467,6 +473,8 @@ def _softmax_mod(name, call, cache, device, seqs, q, scale, mod, sel, n_sel, cap
     batch, T, Hq, d = shape
     if batch != seqs.batch or d != cache.head_dim:
         raise ValueError("q does not fit the batch and the cache")
+    if seqs.device_index != device:
+        raise ValueError("all tensors must be on one device")
     if out.shape != shape or out.dtype != torch.float32:
         raise ValueError("out must be fp32 of q's shape")
     if lse is not None and (lse.shape != shape[:3] or lse.dtype != torch.float32):

@@ -199,3 +199,23 @@ def test_binding_refuses():
         B.ekv_rope_append_q4(cache, seqs, None, B.make_new_tokens(torch.zeros(1, 2, 64), torch.zeros(1, 2, 64)))
     with pytest.raises(ValueError):
         B.ekv_q4_read(cache, seqs, torch.zeros(2, dtype=torch.int32), torch.zeros(1, 2, 64))
+
+
+def test_descriptions_refuse_strided_tables_and_take_single_rows():
+    table = torch.zeros(4, 8, dtype=torch.int32)
+    lens = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        B.make_seqs(table[:, :3], lens)               # a view of a wider table would be read at the wrong places
+    with pytest.raises(ValueError):
+        B.make_seqs(table, torch.zeros(8, dtype=torch.int32)[::2])
+    with pytest.raises(ValueError):
+        B.make_seqs(table, torch.zeros(4, dtype=torch.int32, device="meta"))
+    assert B.make_seqs(table[:, :8], lens).max_pages == 8
+    # one row, or one head: its stride says nothing
+    k = torch.zeros(1, 2, 64).as_strided((1, 2, 64), (1, 64, 1))
+    n = B.make_new_tokens(k, k, torch.zeros(1, 4, 64), torch.zeros(1, 4, 64))
+    assert (n.k_stride, n.v_stride, n.q_stride) == (128, 128, 256)
+    one = torch.zeros(3 * 256).as_strided((3, 1, 64), (256, 1, 1))
+    assert B.make_new_tokens(one, one).k_stride == 256
+    with pytest.raises(ValueError):
+        B.make_new_tokens(*[torch.zeros(3 * 256).as_strided((3, 2, 64), (256, 1, 1))] * 2)
