@@ -243,6 +243,118 @@ __device__ __forceinline__ int ref_distance(float slope, int i, int2 ref) {
   return slope >= 0.f ? max(0, i - ref.y) : abs(i - ref.x);
 }
 
+// Where a CTA's run of the work list starts, and how the list is cut.
+struct Run {
+  long long total;   // tiles of the list
+  long long start;   // the run's first tile, or its piece when the cuts are aligned
+  long long grp_at;  // the first of group grp, in the same count
+  int per;           // tiles of a run, about those of a piece
+  int grp, grp_tiles;  // the group that holds the start (−1: no such run), tiles of each of its units
+  bool aligned;
+};
+
+// Cutting the list into equal runs keeps every CTA equally busy but lets one
+// cross units, which costs it a second set of queries and a second merge;
+// cutting every unit into equal pieces costs nothing while there are CTAs
+// enough, so that comes first.  Every warp works it out by itself, N groups per
+// lane at a time, all their loads first (block-wide scans took 2.4 us of a 24 us
+// call, loads one by one 1.9 of 15).  N = 1: at most 32 groups, without loops; short
+// calls wait for instructions as much as for data, and the same code with N = 4
+// took 0.5 us more of 10 to 20.
+template <int N>
+__device__ __forceinline__ Run find_run(const ModArgs& a, int groups, int mult) {
+  constexpr int kChunk = 32 * N;
+  const int lane = threadIdx.x & 31, bound = N == 1 ? 1 : groups;
+  Run run;
+  int mine[N];  // tiles of groups 32·i + lane of the chunk in work
+  int held = -1;
+  auto load_chunk = [&](int c0) {
+    if (held == c0) return;
+    held = c0;
+    Bounds s[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (N > 1 && c0 + 32 * i >= groups) continue;
+      const int grp = min(c0 + 32 * i + lane, groups - 1);
+      if (a.sel) s[i].L = a.n_sel[grp];
+      else s[i] = load_bounds(a, grp);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      mine[i] = c0 + 32 * i + lane >= groups ? 0
+                : a.sel                      ? selected_tiles(a, s[i].L)
+                                             : max(1, visible_tiles(a, s[i]).n);
+  };
+  auto sum_over_groups = [&](auto value) {  // value(tiles), times the units of a group
+    long long total = 0;
+    for (int c0 = 0; c0 < bound; c0 += kChunk) {
+      load_chunk(c0);
+      int x = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) x += value(mine[i]);
+      // in two halves: 128 long sequences pass 32 bits
+      total += (__reduce_add_sync(0xffffffffu, x & 0xffff) +
+                (static_cast<long long>(__reduce_add_sync(0xffffffffu, x >> 16)) << 16)) * mult;
+    }
+    return total;
+  };
+  const long long total = run.total = sum_over_groups([](int n) { return n; });
+  const int ctas = static_cast<int>(gridDim.x);
+  int per = total < 0x70000000 ? static_cast<int>((static_cast<uint32_t>(total) + ctas - 1) / static_cast<uint32_t>(ctas))
+                               : static_cast<int>((total + ctas - 1) / ctas);
+  per = max(per, a.min_tiles);
+  bool aligned = false;
+  if (static_cast<long long>(groups) * mult <= ctas) {
+    auto fits = [&](int by) {
+      const float inv = 1.f / static_cast<float>(by);
+      return sum_over_groups([inv](int n) { return n > 0 ? piece_count(n, inv) : 0; }) <= ctas;
+    };
+    // what the CTAs of one of equal units would take; else the equal run
+    const float units = static_cast<float>(groups * mult);
+    const float each = floorf(static_cast<float>(ctas) / units + 1e-3f);
+    const int by = max(a.min_tiles, static_cast<int>(ceilf(static_cast<float>(total) / (units * each))));
+    if (by - per <= a.slack_tiles && fits(by)) {
+      aligned = true;
+      per = by;
+    } else {
+      aligned = by != per && fits(per);
+    }
+  }
+  run.aligned = aligned;
+  run.per = per;
+  // the group that holds this CTA's start: counted in pieces, or in tiles
+  run.start = aligned ? blockIdx.x : static_cast<long long>(per) * blockIdx.x;
+  const float inv_per = 1.f / static_cast<float>(per);
+  run.grp_at = 0;
+  run.grp = -1;
+  run.grp_tiles = 0;
+  for (int c0 = 0; c0 < bound && run.grp < 0; c0 += kChunk) {
+    load_chunk(c0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (N > 1 && (run.grp >= 0 || c0 + 32 * i >= groups)) continue;
+      const int len = (aligned && mine[i] > 0 ? piece_count(mine[i], inv_per) : mine[i]) * mult;
+      int up = len;  // inclusive scan over the lanes
+#pragma unroll
+      for (int sh = 1; sh < 32; sh <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, up, sh);
+        if (lane >= sh) up += y;
+      }
+      const int off = run.start - run.grp_at < 0x7fffffff ? static_cast<int>(run.start - run.grp_at) : 0x7fffffff;
+      const uint32_t hit = __ballot_sync(0xffffffffu, up - len <= off && off < up);
+      if (hit) {
+        const int from = __ffs(hit) - 1;
+        run.grp = c0 + 32 * i + from;
+        run.grp_tiles = __shfl_sync(0xffffffffu, mine[i], from);
+        run.grp_at += __shfl_sync(0xffffffffu, up - len, from);
+      } else {
+        run.grp_at += __shfl_sync(0xffffffffu, up, 31);
+      }
+    }
+  }
+  return run;
+}
+
 // NT: groups of 8 query rows per warp.  4 bits at NT = 1: eight warps of at most
 // 128 registers and two tiles a step, since turning codes into numbers keeps the
 // issue slots busy and what is done once per step counts; on 4 × 131,072 tokens 16
@@ -314,97 +426,17 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   }
   grid_dep_enter();
 
-  // This CTA's run of the work list.  Cutting the list into equal runs keeps
-  // every CTA equally busy but lets one cross units, which costs it a second
-  // set of queries and a second merge; cutting every unit into equal pieces
-  // costs nothing while there are CTAs enough, so that comes first.  Every warp
-  // works it out by itself, four groups per lane at a time, all their loads first
-  // (block-wide scans took 2.4 us of a 24 us call, loads one by one 1.9 of 15).
+  // this CTA's run of the work list
   const int mult = a.sel ? 1 : a.Hkv, groups = a.sel ? a.batch * a.Hkv : a.batch;
-  int mine[4];  // tiles of groups 32·i + lane of the chunk in work
-  int held = -1;
-  auto load_chunk = [&](int c0) {
-    if (held == c0) return;
-    held = c0;
-    Bounds s[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (c0 + 32 * i >= groups) continue;
-      const int grp = min(c0 + 32 * i + lane, groups - 1);
-      if (a.sel) s[i].L = a.n_sel[grp];
-      else s[i] = load_bounds(a, grp);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      mine[i] = c0 + 32 * i + lane >= groups ? 0
-                : a.sel                      ? selected_tiles(a, s[i].L)
-                                             : max(1, visible_tiles(a, s[i]).n);
-  };
-  auto sum_over_groups = [&](auto value) {  // value(tiles), times the units of a group
-    long long total = 0;
-    for (int c0 = 0; c0 < groups; c0 += 128) {
-      load_chunk(c0);
-      int x = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x += value(mine[i]);
-      // in two halves: 128 long sequences pass 32 bits
-      total += (__reduce_add_sync(0xffffffffu, x & 0xffff) +
-                (static_cast<long long>(__reduce_add_sync(0xffffffffu, x >> 16)) << 16)) * mult;
-    }
-    return total;
-  };
-  const long long total = sum_over_groups([](int n) { return n; });
-  const int ctas = static_cast<int>(gridDim.x);
-  int per = total < 0x70000000 ? static_cast<int>((static_cast<uint32_t>(total) + ctas - 1) / static_cast<uint32_t>(ctas))
-                               : static_cast<int>((total + ctas - 1) / ctas);
-  per = max(per, a.min_tiles);
-  bool aligned = false;
-  if (static_cast<long long>(groups) * mult <= ctas) {
-    auto fits = [&](int by) {
-      const float inv = 1.f / static_cast<float>(by);
-      return sum_over_groups([inv](int n) { return n > 0 ? piece_count(n, inv) : 0; }) <= ctas;
-    };
-    // what the CTAs of one of equal units would take; else the equal run
-    const float units = static_cast<float>(groups * mult);
-    const float each = floorf(static_cast<float>(ctas) / units + 1e-3f);
-    const int by = max(a.min_tiles, static_cast<int>(ceilf(static_cast<float>(total) / (units * each))));
-    if (by - per <= a.slack_tiles && fits(by)) {
-      aligned = true;
-      per = by;
-    } else {
-      aligned = by != per && fits(per);
-    }
-  }
   if (tid == 0) a.cut[blockIdx.x] = make_int4(0, 0, 0, 0);
-  // the group that holds this CTA's start: counted in pieces, or in tiles
-  const long long start = aligned ? blockIdx.x : static_cast<long long>(per) * blockIdx.x;
+  const Run run = groups <= 32 ? find_run<1>(a, groups, mult) : find_run<4>(a, groups, mult);
+  const bool aligned = run.aligned;
+  const long long total = run.total;
+  const int per = run.per;
   const float inv_per = 1.f / static_cast<float>(per);
-  long long pos = start, grp_at = 0;
-  int grp = -1, grp_tiles = 0;
-  for (int c0 = 0; c0 < groups && grp < 0; c0 += 128) {
-    load_chunk(c0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (grp >= 0 || c0 + 32 * i >= groups) continue;
-      const int len = (aligned && mine[i] > 0 ? piece_count(mine[i], inv_per) : mine[i]) * mult;
-      int up = len;  // inclusive scan over the lanes
-#pragma unroll
-      for (int sh = 1; sh < 32; sh <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, up, sh);
-        if (lane >= sh) up += y;
-      }
-      const int off = start - grp_at < 0x7fffffff ? static_cast<int>(start - grp_at) : 0x7fffffff;
-      const uint32_t hit = __ballot_sync(0xffffffffu, up - len <= off && off < up);
-      if (hit) {
-        const int from = __ffs(hit) - 1;
-        grp = c0 + 32 * i + from;
-        grp_tiles = __shfl_sync(0xffffffffu, mine[i], from);
-        grp_at += __shfl_sync(0xffffffffu, up - len, from);
-      } else {
-        grp_at += __shfl_sync(0xffffffffu, up, 31);
-      }
-    }
-  }
+  long long pos = run.start, grp_at = run.grp_at;
+  int grp = run.grp;
+  const int grp_tiles = run.grp_tiles;
   if (grp < 0) return;  // more CTAs than runs
   const long long end = pos + per < total ? pos + per : total;  // of a run of tiles
 
