@@ -17,10 +17,11 @@
 //
 // Measured (32 query and 8 KV heads of 128): 15k prompt tokens into bf16 pages
 // 70 us, 5.5 TB/s on the bytes they need (0.85 of the measured copy), into 4 bits
-// with 7.7k tokens 62 us, bound by issue (quantising 350 of 780 instructions per
-// token and KV head); the read-back of 100k tokens 97 us, 5.4 TB/s, writes for the
-// most part; one token in each of 64 sequences 5.6 us (4 bits 5.9), the chain
-// length, page, keys, metadata.
+// with 7.7k tokens 51 us, of which the queries take 16, the metadata 9 and the rest
+// is bound by issue and by few warps to hide latencies (520 instructions per token and
+// KV head, issue slots 62% used); the read-back of 100k tokens 95 us, 5.5 TB/s,
+// writes for the most part; one token in each of 64 sequences 5.6 us (4 bits 6.2),
+// the chain length, page, keys, metadata.
 #include "q4.cuh"
 
 namespace ekv {
