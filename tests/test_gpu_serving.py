@@ -642,3 +642,34 @@ def test_appends_and_reads_at_the_last_positions(q4):
         codes, step, _ = unpack(pool, d)
         assert not codes[..., :-1, :].any() and not step[..., :-1].any()
     assert B.ekv_get_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_q4_codes_of_every_scale(d, dtype):
+    """Rows from 1e-36 to 1e37, some far from zero next to their spread: step, zero and
+    codes are those of 64 bits, number for number."""
+    rows, hkv, S = 16 * 37, 2, 16
+    pg = Paged([rows], hkv, d, S, seed=41 + d)
+    scale = 10.0 ** torch.linspace(-36, 37, rows, dtype=torch.float64, device="cuda")[:, None, None]
+    x = [pg.randn(rows, hkv, d, dtype=torch.float64) for _ in range(2)]
+    far = torch.tensor([0.0, 3.0, 200.0, 9e3], dtype=torch.float64, device="cuda")[torch.arange(rows, device="cuda") % 4]
+    k, v = ((t / 8 * scale + far[:, None, None] * scale).to(dtype) for t in x)
+    k[5::7, 0] = k[5::7, 0, :1]                     # rows of one value
+    ok = (k.float().isfinite() & v.float().isfinite()).all()
+    if not ok:                                      # 9e3·1e37 is past fp32
+        k, v = (t.float().clamp(-3e38, 3e38).to(dtype) for t in (k, v))
+    pool = torch.zeros_like(pg.pool_q4())
+    seqs = B.make_seqs(pg.table, pg.seq_lens)
+    B.ekv_rope_append_q4(B.make_cache_q4(pool, d), seqs, None, B.make_new_tokens(
+        k, v, indptr=torch.tensor([0, rows], dtype=torch.int32, device="cuda")))
+    assert B.ekv_get_error() == 0
+    codes, step, zero = unpack(pool, d)             # [phys, Hkv, tile, K/V, 16, d]
+    kv = np64(torch.stack([k, v]))
+    for t in range(rows):
+        page, slot = int(pg.table_h[0, t // S]), t % S
+        for h in range(hkv):
+            for i in range(2):
+                c, st, z = quantise64(kv[i, t, h])
+                at = (page, h, 0, i, slot)
+                assert st == step[at] and z == zero[at] and (c == codes[at]).all(), (t, h, i)
