@@ -219,8 +219,9 @@ __device__ __forceinline__ Tile resolve_tile(const ModArgs& a, const Segment& s,
   const int phys = a.page_table[static_cast<size_t>(s.b) * a.max_pages + lp];
   if (!phys_ok(phys, a.num_phys)) return r;
   r.at = (phys * a.Hkv + s.h) * tpp + part;
+  // (a prefix hides nothing from any row at or behind position 0: with L < T some lie before it)
   const bool whole = j0 >= s.vis.start &&
-                     (j0 + kTile <= s.vis.prefix ||
+                     ((j0 + kTile <= s.vis.prefix && s.vis.L >= a.T) ||
                       (j0 + kTile <= s.vis.L - a.T + 1 && (a.window <= 0 || s.vis.L - 1 - j0 < a.window)));
   r.j0 = j0 | (whole ? 1 : 0) | (j0 + kTile <= s.vis.L - a.T + 1 ? 2 : 0);
   return r;
