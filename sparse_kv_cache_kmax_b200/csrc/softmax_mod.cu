@@ -510,7 +510,10 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   // a lane's share of its query row (row g of each group of 8): bf16 caches, the
   // B fragments; 4 bits, D/4 numbers from D/4·t4
   uint32_t q_raw[NT][KS * 2];
-  auto prologue = [&](const Segment& s) {  // the unit's queries and first copies are on their way
+  // The unit's queries and first copies are on their way.  used: the slots have been
+  // read, and written where masked rows of V were zeroed, since the kernel's start;
+  // that comes before the copies into them.
+  auto prologue = [&](const Segment& s, bool used) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int row = (rg * NT + nt) * 8 + g, rr = row < rows ? row : 0, t = rr >> a.gsh;
@@ -532,7 +535,10 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
     const int nk = stream_steps(s);
     cur = lookup(s, 0);
     const int step = lane / U, sl = ring_at + step < ST ? ring_at + step : ring_at + step - ST;
-    if (rg == 0 && step < ST && step < nk) issue(cur, sl, lane % U);
+    if (rg == 0 && step < ST && step < nk) {
+      if (used) fence_proxy_async_shared();
+      issue(cur, sl, lane % U);
+    }
     if (nk > kSteps - ST) nxt = lookup(s, 1);
   };
   auto stream_sync = [&]() {
@@ -544,7 +550,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
   bool first_segment = true;
   int which = 0;
   __syncthreads();  // barriers initialised
-  prologue(seg);
+  prologue(seg, false);
   if (tid == 0) s_seg[0] = seg;
   __syncthreads();
 
@@ -832,6 +838,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           if (!(seen >> tok & 1u)) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) *chunk(i) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_shared();  // these stores come before the copies that refill the slot
           }
           if (some) {
             bool bad = false;
@@ -1027,6 +1034,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
               *reinterpret_cast<uint4*>(vt + (lane >> 3) * (kTile * 128) + tok * 128 + (lane & 7) * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
           }
+          fence_proxy_async_shared();
           __syncwarp();
         }
       }
@@ -1181,7 +1189,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           seg.vis = visible_tiles(a, load_bounds(a, a.sel ? grp / a.Hkv : grp));
         }
         place();
-        prologue(seg);
+        prologue(seg, true);
         if (tid == 0) s_seg[which ^ 1] = seg;
       }
     }
