@@ -314,7 +314,7 @@ def workspace(nbytes: int, device) -> torch.Tensor:
     """A 256-byte-aligned device scratch buffer of at least nbytes."""
     t = torch.empty(max(int(nbytes), 1) + 256, dtype=torch.uint8, device=device)
     off = (-t.data_ptr()) % 256
-    return t[off: off + max(int(nbytes), 1)]
+    return t[off: off + max(int(nbytes), 1)] if off else t
 
 
 def ekv_workspace_bytes(op, cache, seqs, num_q_heads, cap) -> int:

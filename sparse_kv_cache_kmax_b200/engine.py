@@ -8,6 +8,7 @@ every page or over the top-k ones.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
@@ -48,7 +49,7 @@ class DecodeEngine:
             raise ValueError("invalid decode configuration")
         self.ws = B.workspace(nbytes, dev)
         self.scale = self.params.scale
-        self.mod_ws = {}  # scratch of the masked softmax decode, by query tokens
+        self.mod_bytes = {}  # scratch bytes of the masked softmax decode, by query tokens
 
     @property
     def box(self):
@@ -89,7 +90,9 @@ class DecodeEngine:
         """Softmax decode of the last T tokens of every sequence, q [B, T, Hq, d]
         (rotated), over every page or over the last step's selection, with
         make_score_mod's options (softcap, slopes, window, prefix_lens, starts).
-        Returns (out [B, T, Hq, d], lse [B, T, Hq])."""
+        Returns (out [B, T, Hq, d], lse [B, T, Hq]).  Calls on different streams do
+        not disturb one another; steps share the engine's buffers and want one
+        stream at a time."""
         sel, n_sel, cap = (self.sel, self.n_sel, self.cap) if selected else (None, None, self.max_pages)
         return _softmax(B.ekv_softmax_decode_mod, self, q, sel, n_sel, cap, mod, stream)
 
@@ -118,16 +121,22 @@ class DecodeEngine:
         return a["out"], k
 
 
+_CURRENT = contextlib.nullcontext()  # the current stream as it is (torch.cuda.stream(None) takes 2 us for the same)
+
+
 def _softmax(call, eng, q, sel, n_sel, cap, mod, stream):
-    """One masked softmax decode with an engine's cache, scale and scratch."""
+    """One masked softmax decode with an engine's cache and scale.  The scratch is the
+    call's own, on its stream: calls on two streams, or captured into two graphs,
+    share none, and the allocator orders its reuse."""
     T = q.shape[1]
-    ws = eng.mod_ws.get(T)
-    if ws is None:
+    nbytes = eng.mod_bytes.get(T)
+    if nbytes is None:
         nbytes = B.ekv_softmax_mod_workspace_bytes(eng.d, eng.Hkv, eng.Hq, T)
         if nbytes == 0:
             raise ValueError("unsupported heads or query tokens")
-        ws = eng.mod_ws[T] = B.workspace(nbytes, eng.device)
-    with torch.cuda.stream(stream):
+        eng.mod_bytes[T] = nbytes
+    with _CURRENT if stream is None else torch.cuda.stream(stream):
+        ws = B.workspace(nbytes, eng.device)
         out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
         lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
     call(eng.cache, eng.seqs, q, eng.scale, B.make_score_mod(**mod), sel, n_sel, cap, out, ws, lse=lse, stream=stream)
@@ -153,7 +162,7 @@ class Q4Engine:
         self.scale = float(scale if scale is not None else 1.0 / math.sqrt(self.d))
         self.rope = None if cos_sin is None else B.make_rope(cos_sin, interleaved)
         self.k = None if k is None else min(int(k), self.max_pages)
-        self.mod_ws = {}
+        self.mod_bytes = {}
         if self.k is not None:
             self.ub = torch.empty(self.batch, self.Hkv, self.max_pages, device=dev)
             self.sel = torch.zeros(self.batch, self.Hkv, self.k, dtype=torch.int32, device=dev)
