@@ -407,6 +407,20 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// Extremes that a NaN reaches: a row that holds one has no smallest number, and its
+// step and zero are NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ double min_nan(double a, double b) { return b < a || b != b ? b : a; }
+__device__ __forceinline__ double max_nan(double a, double b) { return b > a || b != b ? b : a; }
 // Step and zero, from the row's extremes: as low halves of two words, whose
 // upper halves differ from them where 64 bits have to decide.
 struct Pair {
@@ -425,22 +439,23 @@ __device__ __forceinline__ Pair step_zero_exact(F exact) {
   double mn = exact(0), mx = mn;
 #pragma unroll
   for (int e = 1; e < 8; ++e) {
-    mn = fmin(mn, exact(e));
-    mx = fmax(mx, exact(e));
+    mn = min_nan(mn, exact(e));
+    mx = max_nan(mx, exact(e));
   }
 #pragma unroll
   for (int o = W / 2; o > 0; o >>= 1) {
-    mn = fmin(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   }
   return Pair{bf16_pair(__double2float_rn((mx - mn) / 15.0), 0.f), bf16_pair(__double2float_rn(mn), 0.f)};
 }
-// The lane's codes, packed; *packed: the row's (step, zero) as they are stored.
+// The lane's codes, packed; *packed: the row's (step, zero) as they are stored.  A row
+// with a NaN or an infinity gets code 0 and a step that is not finite: NaN as a value.
 template <class F>
 __device__ __forceinline__ uint32_t row_codes(const float (&x)[8], Pair p, float err, F exact, uint32_t* packed) {
   float step = bf16_lo(p.step);
   const float zero = bf16_lo(p.zero);
-  if (!(step >= 1e-30f)) step = 0.f;
+  if (step < 1e-30f) step = 0.f;
   // f = (x − zero)/(15·step), clamped to 0 .. 1 as it is formed.  15·f ≤ 15 is off
   // by 15·err·inv, by 2⁻²³ of it for the reciprocal and 2⁻²⁴ for each of 1/15, the
   // product and f (75·2⁻²⁴ < 5e-6), and by 15·2⁻²⁴ of |off| for the rounding of
@@ -580,18 +595,18 @@ __global__ void __launch_bounds__(kThreads, 5) rope_append_q4_kernel(AppendArgs 
         const float zs = z[e] * s[e];
         y[e] = fmaf(x[e], c[e], zs);
         big = fmaxf(big, fabsf(y[e]) + fabsf(zs));
-        kmn = e ? fminf(kmn, y[e]) : y[e];
-        kmx = e ? fmaxf(kmx, y[e]) : y[e];
-        vmn = e ? fminf(vmn, v[e]) : v[e];
-        vmx = e ? fmaxf(vmx, v[e]) : v[e];
+        kmn = e ? min_nan(kmn, y[e]) : y[e];
+        kmx = e ? max_nan(kmx, y[e]) : y[e];
+        vmn = e ? min_nan(vmn, v[e]) : v[e];
+        vmx = e ? max_nan(vmx, v[e]) : v[e];
       }
 #pragma unroll
       for (int o = kLanes / 2; o > 0; o >>= 1) {
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        kmn = fminf(kmn, __shfl_xor_sync(0xffffffffu, kmn, o));
-        kmx = fmaxf(kmx, __shfl_xor_sync(0xffffffffu, kmx, o));
-        vmn = fminf(vmn, __shfl_xor_sync(0xffffffffu, vmn, o));
-        vmx = fmaxf(vmx, __shfl_xor_sync(0xffffffffu, vmx, o));
+        kmn = min_nan(kmn, __shfl_xor_sync(0xffffffffu, kmn, o));
+        kmx = max_nan(kmx, __shfl_xor_sync(0xffffffffu, kmx, o));
+        vmn = min_nan(vmn, __shfl_xor_sync(0xffffffffu, vmn, o));
+        vmx = max_nan(vmx, __shfl_xor_sync(0xffffffffu, vmx, o));
       }
       const float err = a.rot ? big * 0x1.1p-24f : 0.f;
       auto key = [&](int e) {

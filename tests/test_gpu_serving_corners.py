@@ -1,16 +1,18 @@
 """Corners of the serving operators on the GPU against 64-bit references: sequences
-shorter than the query tokens, and many short sequences in one run of a CTA."""
+shorter than the query tokens, many short sequences in one run of a CTA, and numbers
+that are not finite."""
 import numpy as np
 import pytest
 import torch
 
 from sparse_kv_cache_kmax_b200 import binding as B
 
-from serving_helpers import Paged, check_decode, decode64, np64, q4_values
+from serving_helpers import (Paged, check_decode, decode64, np64, q4_values, quantise64, rope_table, rotate64,
+                             unpack)
 from test_gpu_serving import _decode
 
 pytestmark = pytest.mark.gpu
-BF = torch.bfloat16
+BF, F32 = torch.bfloat16, torch.float32
 BOTH = pytest.mark.parametrize("q4", [False, True], ids=["bf16", "q4"])
 
 
@@ -88,3 +90,68 @@ def test_runs_over_many_units_with_masked_tails(G, T, q4):
     assert B.ekv_get_error() == 0
     check_decode(got[0][0][some], got[0][1][some], want)
     assert all(torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1]) for out, lse in got[1:])
+
+
+# ------------------------------------------------------------------ numbers that are not finite
+@pytest.mark.parametrize("rotate", [None, False, True], ids=["plain", "halves", "neighbours"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_4_bit_rows_with_a_number_that_is_not_finite_are_nan(d, dtype, rotate):
+    """One NaN or infinity in a row of K or V, at every lane's place: that row reads back
+    as NaN, step and metadata show it, and the rows beside it are what they would be."""
+    rows, hkv, S, rot = 70, 2, 16, d // 2
+    pg = Paged([rows], hkv, d, S, seed=720 + d)
+    k, v = pg.randn(rows, hkv, d, dtype=dtype), pg.randn(rows, hkv, d, dtype=dtype)
+    table = rope_table(rows, rot)
+    junk = [float("nan"), float("inf"), -float("inf")]
+    hit = np.zeros((2, rows, hkv), bool)
+    for n in range(0, rows, 3):                      # with untouched rows between: two share a warp's step
+        part, h, at = n % 2, (n // 3) % hkv, (n * 13) % d
+        (k, v)[part][n, h, at] = junk[n % 7 % 3]
+        hit[part, n, h] = True
+    pool = torch.zeros_like(pg.pool_q4())
+    box = torch.zeros(hkv, pg.n_phys, 2, d, dtype=BF, device="cuda")
+    mom = torch.zeros_like(box)
+    cache, seqs = B.make_cache_q4(pool, d, box, mom), B.make_seqs(pg.table, pg.seq_lens)
+    indptr = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    B.ekv_rope_append_q4(cache, seqs, None if rotate is None else B.make_rope(table, rotate),
+                         B.make_new_tokens(k, v, indptr=indptr))
+    got = [torch.zeros(rows, hkv, d, device="cuda") for _ in range(2)]
+    B.ekv_q4_read(cache, seqs, indptr, *got)
+    assert B.ekv_get_error() == 0
+    codes, step, zero = unpack(pool, d)
+    x = [np64(k), np64(v)]
+    if rotate is not None:
+        with np.errstate(invalid="ignore"):
+            x[0] = rotate64(x[0], np64(table), np.arange(rows), rotate)
+    for n in range(rows):
+        ph, s = int(pg.table_h[0, n // S]), n % S
+        for h in range(hkv):
+            for part in (0, 1):
+                at = (ph, h, 0, part, s)
+                if hit[part, n, h]:
+                    assert torch.isnan(got[part][n, h]).all(), (part, n, h)
+                    assert not np.isfinite(step[at])
+                else:
+                    c, st, ze = quantise64(x[part][n, h])
+                    assert np.array_equal(codes[at], c) and step[at] == st and zero[at] == ze, (part, n, h)
+    for p in range(pg.pages[0]):                     # the moments of a page that holds such a key are NaN
+        ph = int(pg.table_h[0, p])
+        for h in range(hkv):
+            bad = hit[0, p * S: (p + 1) * S, h].any()
+            assert bool(torch.isnan(mom[h, ph]).all()) == bad and bool(torch.isnan(mom[h, ph]).any()) == bad
+
+
+@pytest.mark.parametrize("part", [0, 1], ids=["key", "value"])
+def test_an_appended_nan_reaches_the_rows_that_see_it(part):
+    """Append, then decode: of two query tokens only the one that sees the NaN token is NaN."""
+    pg = Paged([41], 1, 64, 16, seed=730)
+    k, v = pg.randn(41, 1, 64), pg.randn(41, 1, 64)
+    (k, v)[part][40, 0, 17] = float("nan")
+    pool = torch.zeros_like(pg.pool_q4())
+    indptr = torch.tensor([0, 41], dtype=torch.int32, device="cuda")
+    B.ekv_rope_append_q4(B.make_cache_q4(pool, 64), B.make_seqs(pg.table, pg.seq_lens), None,
+                         B.make_new_tokens(k, v, indptr=indptr))
+    out, _, _ = _decode(pg, pg.randn(1, 2, 4, 64), {}, q4=True, pools=pool)
+    assert torch.isfinite(out[:, 0]).all() and torch.isnan(out[:, 1]).all()
+    assert B.ekv_get_error() == 0
