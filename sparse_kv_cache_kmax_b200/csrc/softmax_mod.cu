@@ -900,9 +900,9 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           }
       } else {
         // w = p·step·2^64, since the codes of V enter as bf16 subnormals n·2⁻¹³³.  The
-        // reference follows p·step as well as p, so that w stays in its range
-        // whatever the steps: it is the largest score plus log2(step), or the
-        // largest score less 32 where steps are below 2^-32.
+        // reference follows p·step and p·(the value of code 8) as well as p, so that w
+        // and both sums stay in their range whatever the steps and values: it is the
+        // largest score plus the largest of log2(step), log2|value| − 64 and −32.
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const uint32_t* pairs = reinterpret_cast<const uint32_t*>(buf + u * (Sh::slot_bytes / U) + 16 * D);
@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
                   w[u][nt][2 * t + e] = p * (vs[u][t] * 0x1p64f);
                   fits = fits && w[u][nt][2 * t + e] <= 0x1p100f;
                 }
-              fits = fits && sum[nt][e] <= 0x1p100f;
+              fits = fits && sum[nt][e] <= 0x1p100f && fabsf(mid[nt][e]) <= 0x1p100f;
             }
           return fits;
         };
@@ -969,7 +969,8 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                   const float x = z[u][nt][2 * t + e];
-                  if (x > -INFINITY) top = fmaxf(top, x + fmaxf(-32.f, __log2f(vs[u][t])));
+                  const float size = fmaxf(__log2f(vs[u][t]), __log2f(fabsf(vmid[u][t])) - 64.f);
+                  if (x > -INFINITY) top = fmaxf(top, x + fminf(64.f, fmaxf(-32.f, size)));
                 }
               move_reference(nt, e, max_over_tokens(top));
             }

@@ -1,6 +1,6 @@
 """Corners of the serving operators on the GPU against 64-bit references: sequences
-shorter than the query tokens, many short sequences in one run of a CTA, and numbers
-that are not finite."""
+shorter than the query tokens, many short sequences in one run of a CTA, numbers that are
+not finite, and sizes near the ends of fp32."""
 import numpy as np
 import pytest
 import torch
@@ -155,3 +155,42 @@ def test_an_appended_nan_reaches_the_rows_that_see_it(part):
     out, _, _ = _decode(pg, pg.randn(1, 2, 4, 64), {}, q4=True, pools=pool)
     assert torch.isfinite(out[:, 0]).all() and torch.isnan(out[:, 1]).all()
     assert B.ekv_get_error() == 0
+
+
+# ------------------------------------------------------------------ sizes near the ends of fp32
+def _pairs(pool, d, part, step, zero):
+    """Sets the (step, zero) of K (part 0) or V (part 1) of every token."""
+    sz = torch.stack([torch.as_tensor(step, device="cuda").expand(16), torch.as_tensor(zero, device="cuda").expand(16)], -1)
+    at = 16 * d + 64 * part
+    pool[..., at: at + 64] = sz.to(BF).contiguous().view(torch.uint8).reshape(64)
+
+
+@pytest.mark.parametrize("T", [1, 4])
+@pytest.mark.parametrize("step,zero", [
+    (0.0, 2.0 ** 126), (0.0, -2.0 ** 97), (2.0 ** -20, 2.0 ** 110), (2.0 ** 60, -2.0 ** 63), (2.0 ** 62, 2.0 ** 120),
+    (0.0, 2.0 ** -100), (2.0 ** -60, 2.0 ** 40)])
+def test_4_bit_values_of_every_size(step, zero, T):
+    """Rows of V far larger than their steps: the weighted mean of finite values is finite."""
+    d = 64
+    pg = Paged([700, 3], 2, d, 16, seed=740)
+    pool = pg.pool_q4()
+    lens = torch.arange(16, device="cuda") % 3 / 8.0 + 0.75  # tokens of a tile differ
+    _pairs(pool, d, 1, step * lens, zero * lens)
+    out, lse, want = _decode(pg, pg.randn(2, T, 8, d), {}, q4=True, pools=pool)
+    assert B.ekv_get_error() == 0
+    check_decode(out, lse, want)
+
+
+@pytest.mark.parametrize("T", [1, 4])
+def test_4_bit_values_of_mixed_sizes(T):
+    """Small and large rows of V side by side, the large ones at the far end."""
+    d = 128
+    pg = Paged([900], 1, d, 16, seed=741)
+    pool = pg.pool_q4()
+    big = torch.tensor(pg.table_h[0, :9].astype(np.int64), device="cuda")
+    part = pool[big].clone()
+    _pairs(part, d, 1, 0.0, 2.0 ** 115)
+    pool[big] = part
+    out, lse, want = _decode(pg, pg.randn(1, T, 4, d), {}, q4=True, pools=pool)
+    assert B.ekv_get_error() == 0
+    check_decode(out, lse, want)
