@@ -351,7 +351,8 @@ EKV_API ekv_status ekv_softmax_decode_mod(const ekv_cache* cache, const ekv_seqs
  * ekv_softmax_decode_q4 — ekv_softmax_decode_mod over a 4-bit cache: K and V
  * are the values the codes stand for (not rounded further).  q is bf16.  Steps
  * are at least 0, and V's below 2^63 (a row that sees a larger one gets NaN or
- * infinities).
+ * infinities).  scale·q, over softcap where there is one of at least 1e-30, is
+ * taken up to 2^110 in size.
  */
 EKV_API ekv_status ekv_softmax_decode_q4(const ekv_cache_q4* cache, const ekv_seqs* seqs, const void* q,
                                          int32_t num_q_heads, int32_t num_q_tokens, float scale,

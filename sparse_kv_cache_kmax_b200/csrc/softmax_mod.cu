@@ -45,6 +45,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr int kModCtas = 296;     // two resident CTAs on each of 148 SMs: one wave
 constexpr float kGrow = 8.0f;     // a score may pass the reference maximum by 2^8 before the state is rescaled
 constexpr float kNoMax = -3e38f;  // before the first score
+constexpr float kHuge = 3.402823466e38f;  // the largest finite number
 
 struct ModArgs {
   const int32_t* page_table;
@@ -588,10 +589,10 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
           qf[ks][nt][1] = q_raw[nt][2 * ks + 1];
         }
       } else {
-        // Scaled by a power of two to a largest number near 2^100 (exact: the codes
-        // enter as subnormals n·2⁻¹³³).  Word w of the lane's share gives the pairs
-        // (8w + i, 8w + i + 4), as the codes do; codes at odd i come 16 times too
-        // large, so their numbers are divided by 16.
+        // Scaled by a power of two to a largest number near 2^120 (exact: the codes
+        // enter as subnormals n·2⁻¹³³, so sums of products stay below 1).  Word w of
+        // the lane's share gives the pairs (8w + i, 8w + i + 4), as the codes do; codes
+        // at odd i come 16 times too large, so their numbers are divided by 16.
         float sum = 0.f, top = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
@@ -603,7 +604,7 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int k = 100 + 127 - static_cast<int>(__float_as_uint(top) >> 23);
+        const int k = 120 + 127 - static_cast<int>(__float_as_uint(top) >> 23);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + max(-126, min(126, k))) << 23);
         uint32_t qh[KS][2];
 #pragma unroll
@@ -624,10 +625,14 @@ __global__ void __launch_bounds__(Shape<D, NT, Q4>::threads, 2)
             qf[ks][nt][1] = qh[ks][1];
           }
         }
-        const float zf = a.cap2 != 0.f ? a.capx : a.scale2, down = zf * 0x1p66f / up * 0x1p67f;
-        qsum[nt][0] = __shfl_sync(0xffffffffu, sum * zf, 8 * t4);
-        qsum[nt][1] = __shfl_sync(0xffffffffu, sum * zf, 8 * t4 + 4);
-        const float c8 = sum * up * -0x1p-65f * 0x1p-65f;
+        // zf·2^133/up: a factor past the ends of fp32 (tiny caps, zero queries) stays
+        // finite, since it may meet a sum or a step of 0
+        const float zf = a.cap2 != 0.f ? a.capx : a.scale2;
+        const float down = fminf(kHuge, zf * (0x1p66f / up) * 0x1p67f);
+        const float qs = fabsf(sum) <= kHuge ? fmaxf(-kHuge, fminf(kHuge, sum * zf)) : sum;
+        qsum[nt][0] = __shfl_sync(0xffffffffu, qs, 8 * t4);
+        qsum[nt][1] = __shfl_sync(0xffffffffu, qs, 8 * t4 + 4);
+        const float c8 = sum * (up * -0x1p-65f) * 0x1p-65f;
         qc[nt][0] = qc[nt][2] = __shfl_sync(0xffffffffu, c8, 8 * t4);
         qc[nt][1] = qc[nt][3] = __shfl_sync(0xffffffffu, c8, 8 * t4 + 4);
         qdown[nt][0] = __shfl_sync(0xffffffffu, down, 8 * t4);
@@ -1461,7 +1466,8 @@ cudaError_t launch_softmax_mod(const ekv_cache& c, const void* pool, const ekv_s
   a.cap = cap;
   a.min_tiles = pool ? 8 : 4;
   a.slack_tiles = pool ? 32 : 12;
-  a.scale2 = scale * kLog2e;
+  auto finite = [](float x) { return x < kHuge ? x : kHuge; };  // so that a sum of 0 stays 0
+  a.scale2 = finite(scale * kLog2e);
   if (mod != nullptr) {
     a.slopes = mod->slopes;
     a.prefix_lens = mod->prefix_lens;
@@ -1469,7 +1475,7 @@ cudaError_t launch_softmax_mod(const ekv_cache& c, const void* pool, const ekv_s
     a.window = mod->window;
     // a cap of 1e30 changes no score in fp32; under 1e-30 scores are ±cap or 0
     if (mod->softcap > 0.f && mod->softcap < 1e30f) {
-      a.capx = scale / fmaxf(mod->softcap, 1e-30f);
+      a.capx = finite(scale / fmaxf(mod->softcap, 1e-30f));
       a.cap2 = mod->softcap * kLog2e;
     }
   }

@@ -194,3 +194,41 @@ def test_4_bit_values_of_mixed_sizes(T):
     out, lse, want = _decode(pg, pg.randn(1, T, 4, d), {}, q4=True, pools=pool)
     assert B.ekv_get_error() == 0
     check_decode(out, lse, want)
+
+
+@BOTH
+@pytest.mark.parametrize("cap,scale", [(1e-37, None), (1e-25, None), (1e-20, 1.0), (3.0, 1e30), (1e-30, 1e10), (0.0, 1e38)])
+def test_small_caps_and_large_scales_with_scores_of_zero(cap, scale, q4):
+    """A query of zeros and keys of zeros score 0 exactly, however large the factor."""
+    d = 64
+    pg = Paged([200, 40], 1, d, 16, seed=750)
+    pools = pg.pool_q4() if q4 else pg.pools()
+    q = pg.randn(2, 1, 4, d)
+    q[:, :, 1] = 0
+    q[:, :, 3, ::2] = 0
+    if scale is not None and scale > 1e9:            # larger scores would be decided by the signs of sums near 0
+        q.zero_()
+    ph = torch.tensor(pg.table_h[0, 2:5].astype(np.int64), device="cuda")
+    if q4:
+        part = pools[ph].clone()
+        part[..., : 8 * d] = 0
+        _pairs(part, d, 0, 0.0, 0.0)
+        pools[ph] = part
+    else:
+        pools[0][ph] = 0
+    out, lse, want = _decode(pg, q, {"cap": cap}, q4=q4, pools=pools, scale=scale)
+    assert B.ekv_get_error() == 0
+    assert torch.isfinite(out).all()
+    check_decode(out, lse, want)
+
+
+@pytest.mark.parametrize("G", [4, 16])
+def test_large_queries_against_small_4_bit_keys(G):
+    d = 128
+    pg = Paged([300, 5], 1, d, 16, seed=751)
+    pool = pg.pool_q4()
+    by = 0.75 + torch.arange(16, device="cuda") % 3 / 8.0
+    _pairs(pool, d, 0, 2.0 ** -98 * by, -2.0 ** -95 * by)
+    out, lse, want = _decode(pg, (pg.randn(2, 1, G, d).float() * 2.0 ** 97).to(BF), {}, q4=True, pools=pool)
+    assert B.ekv_get_error() == 0
+    check_decode(out, lse, want)
