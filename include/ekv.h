@@ -334,10 +334,10 @@ typedef struct {
  * mod may be NULL (causal, nothing else).  sel / n_sel / cap as
  * ekv_softmax_decode; a page named twice counts twice.  Only pages with a
  * visible token are read.  A row without a visible token (also L_b = 0, an
- * idle slot, and i < 0) gives out 0 and lse −inf.  K and V of tokens that a
- * row does not see never reach it, NaN and infinities included.  bf16 caches,
- * G·T ≤ 64, max_pages·S·Hkv < 2³⁰ (cap·S < 2³⁰ with sel); anything else returns
- * EKV_ERR_UNSUPPORTED.  ws:
+ * idle slot, and i < 0), or with scores of −inf alone, gives out 0 and lse −inf.
+ * K and V of tokens that a row does not see never reach it, NaN and infinities
+ * included.  bf16 caches, G·T ≤ 64, max_pages·S·Hkv < 2³⁰ (cap·S < 2³⁰ with
+ * sel); anything else returns EKV_ERR_UNSUPPORTED.  ws:
  * ekv_softmax_mod_workspace_bytes() bytes, 256-byte aligned, for one call at a
  * time; nothing in it outlives the call.
  */

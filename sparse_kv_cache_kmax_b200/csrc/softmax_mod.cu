@@ -44,8 +44,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
 constexpr int kModCtas = 296;     // two resident CTAs on each of 148 SMs: one wave
 constexpr float kGrow = 8.0f;     // a score may pass the reference maximum by 2^8 before the state is rescaled
-constexpr float kNoMax = -3e38f;  // before the first score
 constexpr float kHuge = 3.402823466e38f;  // the largest finite number
+constexpr float kNoMax = -kHuge;  // before the first score
 
 struct ModArgs {
   const int32_t* page_table;

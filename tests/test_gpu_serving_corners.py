@@ -232,3 +232,31 @@ def test_large_queries_against_small_4_bit_keys(G):
     out, lse, want = _decode(pg, (pg.randn(2, 1, G, d).float() * 2.0 ** 97).to(BF), {}, q4=True, pools=pool)
     assert B.ekv_get_error() == 0
     check_decode(out, lse, want)
+
+
+@BOTH
+def test_scores_near_the_lowest_of_fp32_still_count(q4):
+    """Tokens alike at a score below -3e38 in base 2: their softmax is their mean all the same."""
+    d, lens = 64, [1, 40]
+    pg = Paged(lens, 1, d, 16, seed=760)
+    pools = pg.pool_q4() if q4 else pg.pools()
+    q = torch.zeros(2, 1, 4, d, device="cuda", dtype=BF)
+    q[..., 0] = 2.0 ** 64
+    low = -1.296875 * 2.0 ** 63                      # the score: -2.2e38, times log2(e) -3.18e38
+    if q4:
+        _pairs(pools, d, 0, 0.0, low)
+    else:
+        pools[0][:] = 0
+        pools[0][..., 0] = low
+    out, lse = torch.empty(2, 1, 4, d, device="cuda"), torch.empty(2, 1, 4, device="cuda")
+    ws = B.workspace(B.ekv_softmax_mod_workspace_bytes(d, 1, 4, 1), "cuda")
+    call = B.ekv_softmax_decode_q4 if q4 else B.ekv_softmax_decode_mod
+    call(B.make_cache_q4(pools, d) if q4 else B.make_cache(*pools), B.make_seqs(pg.table, pg.seq_lens), q, 1.0, None,
+         None, None, pg.max_pages, out, ws, lse=lse)
+    assert B.ekv_get_error() == 0
+    V = q4_values(pools, d)[1] if q4 else np64(pools[1])
+    for b, L in enumerate(lens):
+        rows = V[pg.table_h[b, : pg.pages[b]], 0].reshape(-1, d)[:L]
+        # equal weights: sums of L and of L products round by 2**-24 each, and so does the quotient
+        assert (np.abs(np64(out[b, 0]) - rows.mean(0)) <= (L + 2) * 2.0 ** -23 * np.abs(rows).max()).all()
+        assert (np.abs(np64(lse[b]) / (2.0 ** 64 * low) - 1) <= 4 * 2.0 ** -24).all()
