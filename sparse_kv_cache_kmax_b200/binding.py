@@ -283,6 +283,8 @@ def make_score_mod(softcap=0.0, slopes=None, window=0, prefix_lens=None, starts=
     for t, dt in ((slopes, torch.float32), (prefix_lens, torch.int32), (starts, torch.int32)):
         if t is not None and (t.dtype != dt or t.dim() != 1 or not t.is_contiguous()):
             raise ValueError("slopes must be fp32 [Hq], prefix_lens and starts int32 [batch]")
+    if not 0 <= int(window or 0) < 2 ** 31:
+        raise ValueError("window must be 0 (none) or a positive 32-bit number")
     keep = [t for t in (slopes, prefix_lens, starts) if t is not None]
     if keep:
         _same_device(*keep)
