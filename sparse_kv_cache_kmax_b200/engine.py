@@ -104,12 +104,14 @@ class DecodeEngine:
         Bsz, Hkv, P = self.batch, self.Hkv, self.max_pages
         dev = self.device
         if not hasattr(self, "_ad"):
-            ws = B.workspace(B.ekv_workspace_bytes(B.EKV_OP_DECODE_ADAPTIVE, self.cache, self.seqs, self.Hq, P), dev)
-            self._ad = dict(sel=torch.empty(Bsz * Hkv * P, dtype=torch.int32, device=dev),
-                            n=torch.zeros(Bsz, Hkv, dtype=torch.int32, device=dev),
-                            out=torch.zeros(Bsz, self.Hq, self.d, device=dev),
-                            tau=torch.zeros(Bsz, self.Hq, device=dev),
-                            cert=torch.zeros(Bsz, self.Hq, dtype=torch.int32, device=dev), ws=ws)
+            nbytes = B.ekv_workspace_bytes(B.EKV_OP_DECODE_ADAPTIVE, self.cache, self.seqs, self.Hq, P)
+            with _on(stream):  # the zeros come first on it, and no other stream's freed memory is written
+                self._ad = dict(sel=torch.empty(Bsz * Hkv * P, dtype=torch.int32, device=dev),
+                                n=torch.zeros(Bsz, Hkv, dtype=torch.int32, device=dev),
+                                out=torch.zeros(Bsz, self.Hq, self.d, device=dev),
+                                tau=torch.zeros(Bsz, self.Hq, device=dev),
+                                cert=torch.zeros(Bsz, self.Hq, dtype=torch.int32, device=dev),
+                                ws=B.workspace(nbytes, dev))
         a = self._ad
         if k_new is not None and self.rope is not None:
             q = self.append(k_new, v_new, q, stream=stream)
@@ -121,7 +123,12 @@ class DecodeEngine:
         return a["out"], k
 
 
-_CURRENT = contextlib.nullcontext()  # the current stream as it is (torch.cuda.stream(None) takes 2 us for the same)
+_CURRENT = contextlib.nullcontext()
+
+
+def _on(stream):
+    """The stream as the current one; None: the current one as it is (torch.cuda.stream(None) takes 2 us for that)."""
+    return _CURRENT if stream is None else torch.cuda.stream(stream)
 
 
 def _softmax(call, eng, q, sel, n_sel, cap, mod, stream):
@@ -135,7 +142,7 @@ def _softmax(call, eng, q, sel, n_sel, cap, mod, stream):
         if nbytes == 0:
             raise ValueError("unsupported heads or query tokens")
         eng.mod_bytes[T] = nbytes
-    with _CURRENT if stream is None else torch.cuda.stream(stream):
+    with _on(stream):
         ws = B.workspace(nbytes, eng.device)
         out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
         lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)

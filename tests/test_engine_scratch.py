@@ -71,3 +71,26 @@ def test_unsupported_query_tokens_are_refused_every_time(calls):
     for _ in range(2):
         with pytest.raises(ValueError):
             run(9, None)
+
+
+def test_the_adaptive_decodes_buffers_belong_to_the_first_calls_stream(monkeypatch):
+    on, made = ["current"], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        on.append(on[-1] if s is None else s)
+        yield
+        on.pop()
+
+    for name in ("empty", "zeros"):
+        def note(*a, make=getattr(torch, name), **kw):
+            made.append(on[-1])
+            return make(*a, **kw)
+        monkeypatch.setattr(torch, name, note)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(B, "ekv_decode_adaptive", lambda *a: 1)
+    pools = [torch.randn(4, 1, 16, 64).bfloat16() for _ in range(2)]
+    eng = E.DecodeEngine(*pools, torch.arange(4, dtype=torch.int32)[None], torch.tensor([50], dtype=torch.int32), 4, k=2)
+    made.clear()
+    eng.decode_adaptive(torch.randn(1, 4, 64).bfloat16(), stream="side")
+    assert made and set(made) == {"side"}
