@@ -268,6 +268,8 @@ EKV_API ekv_status ekv_rope_append(const ekv_cache* cache, const ekv_seqs* seqs,
  * (coordinate 2i in the low half of byte i), the V codes [16, d/2], 16 pairs
  * (step, zero) in bf16 for K, 16 for V.  A row x of d numbers has
  *   zero = bf16(min x), step = bf16((max x − min x)/15) (0 below 1e-30),
+ * (of the numbers in 64 bits; bf16() rounds them to fp32 and from there to bf16,
+ * so a number within 2^-24 of a border between two bf16 numbers counts as on it)
  *   n_j = clamp(round((x_j − zero)/step), 0, 15)   (halves to the even code),
  * and stands for zero + step·n_j.  A row with a NaN or an infinity stands for
  * NaN throughout (its codes are 0, its step is not finite); in metadata, as in
@@ -336,8 +338,10 @@ typedef struct {
  * visible token are read.  A row without a visible token (also L_b = 0, an
  * idle slot, and i < 0), or with scores of −inf alone, gives out 0 and lse −inf.
  * K and V of tokens that a row does not see never reach it, NaN and infinities
- * included.  bf16 caches, G·T ≤ 64, max_pages·S·Hkv < 2³⁰ (cap·S < 2³⁰ with
- * sel); anything else returns EKV_ERR_UNSUPPORTED.  ws:
+ * included.  Sums of p·v are held in fp32 with p up to 2^8, so a bf16 cache's
+ * |v| times the visible tokens stays below 2^119.  bf16 caches, G·T ≤ 64,
+ * max_pages·S·Hkv < 2³⁰ (cap·S < 2³⁰ with sel); anything else returns
+ * EKV_ERR_UNSUPPORTED.  ws:
  * ekv_softmax_mod_workspace_bytes() bytes, 256-byte aligned, for one call at a
  * time; nothing in it outlives the call.
  */

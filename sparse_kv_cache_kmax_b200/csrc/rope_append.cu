@@ -447,6 +447,7 @@ __device__ __forceinline__ Pair step_zero_exact(F exact) {
     mn = min_nan(mn, __shfl_xor_sync(0xffffffffu, mn, o));
     mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   }
+  // to fp32 and from there to bf16, as the format says
   return Pair{bf16_pair(__double2float_rn((mx - mn) / 15.0), 0.f), bf16_pair(__double2float_rn(mn), 0.f)};
 }
 // The lane's codes, packed; *packed: the row's (step, zero) as they are stored.  A row

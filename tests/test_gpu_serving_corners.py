@@ -260,3 +260,26 @@ def test_scores_near_the_lowest_of_fp32_still_count(q4):
         # equal weights: sums of L and of L products round by 2**-24 each, and so does the quotient
         assert (np.abs(np64(out[b, 0]) - rows.mean(0)) <= (L + 2) * 2.0 ** -23 * np.abs(rows).max()).all()
         assert (np.abs(np64(lse[b]) / (2.0 ** 64 * low) - 1) <= 4 * 2.0 ** -24).all()
+
+
+def test_4_bit_steps_and_zeros_are_rounded_by_way_of_fp32():
+    """2^-26 beyond the middle of two bf16 numbers: on it in fp32, so to the even one."""
+    d = 64
+    pg = Paged([1], 1, d, 16, seed=780)
+    v = torch.linspace(0, 15, d, dtype=F32, device="cuda")[None, None].clone()
+    v[0, 0, 0], v[0, 0, 1] = -15 * 2.0 ** -26, 15 + 15 / 256           # (max - min)/15 = 1 + 2^-8 + 2^-26
+    k = torch.zeros_like(v)
+    k[0, 0, 0], k[0, 0, d // 2] = -(1 + 2.0 ** -8), 1                  # turned: min = -(1 + 2^-8 + 2^-26)
+    table = torch.zeros(1, d, device="cuda")
+    table[:, : d // 2] = 1
+    table[0, d // 2] = 2.0 ** -26
+    pool = torch.zeros_like(pg.pool_q4())
+    B.ekv_rope_append_q4(B.make_cache_q4(pool, d), B.make_seqs(pg.table, pg.seq_lens), B.make_rope(table),
+                         B.make_new_tokens(k, v))
+    codes, step, zero = unpack(pool, d)
+    ph = int(pg.table_h[0, 0])
+    assert step[ph, 0, 0, 1, 0] == 1.0 and zero[ph, 0, 0, 0, 0] == -1.0
+    for part, row in ((0, rotate64(np64(k), np64(table), np.array([0]), False)[0, 0]), (1, np64(v)[0, 0])):
+        c, st, ze = quantise64(row)
+        assert np.array_equal(codes[ph, 0, 0, part, 0], c) and step[ph, 0, 0, part, 0] == st and zero[ph, 0, 0, part, 0] == ze
+    assert B.ekv_get_error() == 0
