@@ -15,9 +15,10 @@
 // sequence never reach the next one's, and ⌊rows/S⌋ + 2·batch items are enough
 // without a prefix sum over the batch.
 //
-// Measured (32 query and 8 KV heads of 128): 15k prompt tokens into bf16 pages
-// 70 us, 5.5 TB/s on the bytes they need (0.85 of the measured copy), into 4 bits
-// with 7.7k tokens 51 us, of which the queries take 16, the metadata 9 and the rest
+// Measured on the device, in a captured graph (32 query and 8 KV heads of 128): 15k
+// prompt tokens into bf16 pages 70 us, 5.5 TB/s on the bytes they need (0.85 of the
+// measured copy; as calls, by the wall clock, 72 us and 0.82), into 4 bits with 7.7k
+// tokens 51 us, of which the queries take 16, the metadata 9 and the rest
 // is bound by issue and by few warps to hide latencies (520 instructions per token and
 // KV head, issue slots 62% used); the read-back of 100k tokens 95 us, 5.5 TB/s,
 // writes for the most part; one token in each of 64 sequences 5.6 us (4 bits 6.2),
@@ -59,9 +60,9 @@ template <class A>
 __device__ bool page_item(const A& a, int item, PageItem* out) {
   int b = item, row0 = item, n = 1, k = 0, L;
   if (a.indptr != nullptr) {
-    // greatest b with base(b) ≤ item, 32 probes at a time; the last probes bring
-    // the sequence's rows and length along, so that two dependent loads (these,
-    // and the page table's) lead to the page
+    // greatest b with base(b) ≤ item, 32 probes at a time: ⌈log32(batch)⌉ rounds, of
+    // which the last brings the sequence's rows and length along, then the page
+    // table's load (without indptr: the length, then the table)
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = a.batch;
     for (;;) {
@@ -324,8 +325,8 @@ __device__ __forceinline__ void column_meta(F value, int n, float* mx, float* mn
 }
 
 // grid: (items, CTAs for K and V, then as many for the queries); a CTA takes
-// a.heads KV heads in turn: the lookup of its page costs four dependent loads,
-// which one head of a prompt's page does not pay for.
+// a.heads KV heads in turn: the lookup of its page is a chain of dependent loads
+// (page_item), which one head of a prompt's page does not pay for.
 template <typename T, int D, int S>
 __global__ void __launch_bounds__(kThreads, 5) rope_append_kernel(AppendArgs a) {
   grid_dep_enter();

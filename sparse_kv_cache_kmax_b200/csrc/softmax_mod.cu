@@ -23,14 +23,14 @@
 // tile and stays far below the time the tile's bytes take.
 //
 // bf16 is bound by HBM, 512 bytes per (token, KV head): 4 sequences of 131,072
-// tokens with 8 KV heads of 4 query heads take 323 us, 6.65 TB/s, as fast as the
+// tokens with 8 KV heads of 4 query heads take 322 us, 6.66 TB/s, as fast as the
 // measured copy (6.55); 64 ragged ones of 4k to 16k tokens 402 us, 6.63 TB/s.
-// 4 bits need 136 bytes and are bound by issue: the same contexts take 179 us,
-// 3.2 TB/s (0.48), at 420 warp instructions per tile (88 to unpack codes, 33
+// 4 bits need 136 bytes and are bound by issue: the same contexts take 178 us,
+// 3.2 TB/s (0.49), at 426 warp instructions per tile (88 to unpack codes, 33
 // tensor products, 32 adds of products, the softmax and its three-part weights)
-// and 0.6 issued per cycle and scheduler.  Short calls are bound by the chain of
-// dependent steps from the lengths to the merge, and by fetching their code: 14 us for
-// 2k tokens.
+// and 0.6 issued per cycle and scheduler; all of this with up to 8 query rows.
+// Short calls are bound by fetching their code, and by the chain of dependent
+// steps from the lengths to the merge: 14 us for 2k tokens.
 #include <cuda.h>
 
 #include <atomic>

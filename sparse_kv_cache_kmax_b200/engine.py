@@ -154,7 +154,8 @@ class Q4Engine:
     """A decode session over a cache held in 4 bits.  pool: uint8 [num_phys, Hkv,
     S/16, B.q4_record_bytes(d)] (``Q4Engine.new_pool``); the engine owns the
     metadata of its pages, so a step can pick the k pages with the largest
-    bounding-box scores first."""
+    bounding-box scores first.  It has metadata of the pages that its own appends
+    touched: with k, a pool starts empty."""
 
     def __init__(self, pool, head_dim, page_table, seq_lens, num_q_heads, *, k=None, scale=None, cos_sin=None,
                  interleaved=False):
