@@ -269,15 +269,14 @@ EKV_API ekv_status ekv_rope_append(const ekv_cache* cache, const ekv_seqs* seqs,
  * (coordinate 2i in the low half of byte i), the V codes [16, d/2], 16 pairs
  * (step, zero) in bf16 for K, 16 for V.  A row x of d numbers has
  *   zero = bf16(min x), step = bf16((max x − min x)/15) (0 below 1e-30),
- * (of the numbers in 64 bits; bf16() rounds them to fp32 and from there to bf16,
- * so a number within 2^-24 of a border between two bf16 numbers counts as on it)
  *   n_j = clamp(round((x_j − zero)/step), 0, 15)   (halves to the even code),
- * and stands for zero + step·n_j.  A row with a NaN or an infinity stands for
- * NaN throughout (its codes are 0, its step is not finite); in metadata, as in
- * ekv_cache's, the extremes pass over NaN and the moments do not.
- * box and mom as in ekv_cache, always bf16,
- * over the values the codes stand for; k_max is rounded up and k_min down, so
- * the bounding-box bound stays a bound.  To score pages, pass an ekv_cache of
+ * and stands for zero + step·n_j.  bf16() takes the numbers in 64 bits and rounds
+ * them to fp32, and from there to bf16, so one within 2^-24 of the middle of two
+ * bf16 numbers counts as on it.  A row with a NaN or an infinity stands for NaN
+ * throughout (its codes are 0, its step is not finite); in metadata, as in
+ * ekv_cache's, the extremes pass over NaN and the moments do not.  box and mom as
+ * in ekv_cache, always bf16, over the values the codes stand for; k_max is
+ * rounded up and k_min down, so the bounding-box bound stays a bound.  To score pages, pass an ekv_cache of
  * dtype EKV_BF16 with the same sizes, box and mom to ekv_score_pages or
  * ekv_select_gauss (they read no K).
  */
